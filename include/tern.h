@@ -461,6 +461,186 @@ tern_status tern_attention_decode_q4_0(const float *q, int32_t Hq, const tern_kv
                                        void *stream);
 
 /*
+ * Rotary position embedding with one to three position axes (the pages have
+ * no counterpart; a model that decodes text, image and video tokens rotates
+ * each head's query and key by the token's position, one axis for text, time /
+ * height / width for images and video).  The first rot_dim elements of a head
+ * form rot_dim / 2 pairs; pair i belongs to the axis of its section (the first
+ * section[0] pairs to axis 0, the next section[1] to axis 1, ...) and turns by
+ * the angle of that axis' position:
+ *   (c, s) = table[pos[axis(i)][t]][i],  y0 = x0 c - x1 s,  y1 = x1 c + x0 s,
+ * every product, sum and difference rounded to fp32 (no fused multiply-add),
+ * so the result is reproducible bit for bit.  Elements from rot_dim on are
+ * copied.  Pair i is (i, i + rot_dim/2), or (2i, 2i + 1) with
+ * TERN_ROPE_INTERLEAVED; TERN_ROPE_INVERSE turns by the negative angle (the
+ * inverse, and with it the gradient, of the rotation).
+ */
+#define TERN_ROPE_INTERLEAVED 1
+#define TERN_ROPE_INVERSE 2
+typedef struct tern_rope_plan {
+    const float *table; /* device, 16-byte aligned: (cos, sin) [n_pos][rot_dim/2][2] */
+    int32_t n_pos;      /* positions in the table */
+    int32_t rot_dim;    /* rotated elements of a head: a multiple of 8, 8..D */
+    int32_t axes;       /* position axes, 1..3 */
+    int32_t section[3]; /* pairs of each axis, summing to rot_dim / 2; 0 for unused axes */
+    int32_t flags;      /* TERN_ROPE_* or 0 */
+    int32_t reserved;   /* must be 0 */
+} tern_rope_plan;
+
+/* Fills a table of tern_rope_plan: the angle of position p and pair i is
+ * p * scale * theta^(-2i / rot_dim), formed in fp64, its cosine and sine
+ * rounded to fp32 (within one rounding error of fp32; a caller with other
+ * frequencies writes its own table).  table: device, 16-byte aligned,
+ * n_pos * rot_dim floats.  Errors: TERN_EINVAL for n_pos < 1, a rot_dim that
+ * is no positive multiple of 8, a theta or scale that is not finite and
+ * positive, a bad pointer; TERN_ECUDA when the launch fails. */
+tern_status tern_rope_table(double theta, double scale, int32_t rot_dim, int32_t n_pos, float *table,
+                            void *stream);
+
+/*
+ * Rotates T token rows of H heads (before tern_kv_append_q4_0 and
+ * tern_attention_decode_q4_0, which apply no rotation; the paged append below
+ * rotates on its own).
+ *  x: device fp32, head h of row t at x + t * ldx + h * D; y alike (ldy); both
+ *  16-byte aligned, ldx and ldy multiples of 4, >= H * D; y may equal x (with
+ *  ldy = ldx), and must not overlap it otherwise.
+ *  pos: device int32 [axes][T].  D: a multiple of 8, 8..512.
+ *  d_invalid: optional device int32 counter (may be NULL): the number of rows
+ *  with a position outside [0, n_pos) is added to it; their y is 0.
+ * T = 0 is a call that does nothing.  Errors: TERN_EINVAL for a bad plan, bad
+ * shapes, strides or pointers, TERN_ECUDA when the launch fails.
+ */
+tern_status tern_rope(const tern_rope_plan *rope, const int32_t *pos, int32_t T, int32_t H, int32_t D,
+                      const float *x, int32_t ldx, float *y, int32_t ldy, int32_t *d_invalid,
+                      void *stream);
+
+/*
+ * A paged KV cache of one layer in 8 bits (the pages cache K and V in Q4_0 and
+ * note that the context's KV memory, not the weights, decides what fits: this
+ * is the 8-bit form for many sequences).  A page holds page_size tokens of
+ * every KV head; 16 consecutive tokens of a page (a block) and one KV head
+ * share a scale, one for K and one for V, value = code * scale:
+ *   k_codes[((page * Hkv + g) * page_size + slot) * D + d]   8-bit codes,
+ *   k_scales[(page * Hkv + g) * (page_size/16) + slot / 16]  fp32 scales,
+ * and v_codes / v_scales alike.  Codes are int8 (TERN_KV_INT8, -127..127) or
+ * fp8 e4m3 (TERN_KV_E4M3, largest 448).  All device memory owned by the
+ * caller; codes 16-byte aligned, scales 4-byte aligned.  This build takes
+ * D = 128.
+ */
+#define TERN_KV_INT8 0
+#define TERN_KV_E4M3 1
+#define TERN_KV_BLOCK 16
+typedef struct tern_paged_cache {
+    int32_t kind;       /* TERN_KV_INT8 or TERN_KV_E4M3 */
+    int32_t Hkv;        /* KV heads */
+    int32_t D;          /* head dimension (128) */
+    int32_t page_size;  /* tokens per page: a multiple of 16, 16..4096 */
+    int32_t n_pages;    /* pages the arrays hold */
+    int32_t reserved;   /* must be 0 */
+    uint8_t *k_codes;
+    float *k_scales;
+    uint8_t *v_codes;
+    float *v_scales;
+} tern_paged_cache;
+
+/*
+ * A batch of B sequences over a paged cache.  Rows [row_start[b],
+ * row_start[b+1]) of a call's buffers belong to sequence b: its last tokens,
+ * row row_start[b+1] - 1 being token ctx[b] - 1.  Token j of sequence b lies
+ * in page pages[b * pages_ld + j / page_size].  A sequence may have no rows.
+ * The arrays are device memory and read by the kernels, so a captured graph
+ * serves changing lengths; T, and not the arrays, bounds every access to the
+ * rows: rows from T on, and rows from row_start[B] on, are neither read nor
+ * written.  max_rows and max_ctx only steer the choice of a kernel and its
+ * split (a larger or smaller sequence is still computed right).
+ */
+typedef struct tern_paged_batch {
+    int32_t B;                /* sequences, 1..4096 */
+    int32_t T;                /* rows of the call's buffers, >= 0 */
+    int32_t max_rows;         /* about the most rows of a sequence, >= 1 */
+    int32_t max_ctx;          /* about the most tokens of a sequence, >= 1 */
+    const int32_t *row_start; /* device int32 [B + 1], nondecreasing from 0 */
+    const int32_t *ctx;       /* device int32 [B]: tokens of each sequence, its rows included */
+    const int32_t *pages;     /* device int32 [B][pages_ld] */
+    int32_t pages_ld;         /* entries of a sequence in `pages`, >= 1 */
+    int32_t reserved;         /* must be 0 */
+} tern_paged_batch;
+
+/*
+ * Rotates the queries and appends the rotated keys and the values of a
+ * batch's rows to the cache, in one launch.
+ *  q, k, v: device fp32 rows of Hq / Hkv / Hkv heads of D (head h of row t at
+ *  q + t * ldq + h * D; the parts of a QKV projection's output), 16-byte
+ *  aligned, strides multiples of 4; q_out likewise, may equal q (with ldqo =
+ *  ldq).  pos: device int32 [axes][T], the rotary positions, which may differ
+ *  from the tokens' places in the cache.
+ * Quantisation of a block of 16 tokens and one KV head, K after its rotation:
+ *  the scale is the least power of two s = 2^e, -100 <= e <= 120, with
+ *  max |x| <= 127 s (int8) or 448 s (e4m3) over the block's new tokens; a
+ *  block that holds earlier tokens keeps max(its old scale, s).  code =
+ *  x / scale, to int8 rounded half to even, to e4m3 by its conversion.  When
+ *  a block's scale grows, its earlier codes are rescaled (code * old / new,
+ *  rounded alike): powers of two keep e4m3 codes exact (but for subnormals)
+ *  and the error of an int8 value at most one step of the final scale, in
+ *  whatever portions the tokens arrived.  Inputs must be finite.
+ *  Codes of the block's later slots, and all other blocks, stay as they were.
+ *  d_invalid: optional device int32 counter (may be NULL): rows whose
+ *  position lies outside the table (their q_out is 0, and K and V are
+ *  appended as 0) or whose token has no valid page (nothing is appended; q_out
+ *  is rotated as usual) are counted in it.
+ * Two sequences of one call must not append into the same block (pages may be
+ * shared as long as only one sequence writes them).  T = 0 does nothing.
+ * Errors: TERN_EINVAL for a bad plan, batch or cache, bad shapes, strides or
+ * pointers, TERN_EUNSUPPORTED for D != 128, TERN_ECUDA.
+ */
+tern_status tern_kv_append_paged(const float *q, int32_t ldq, int32_t Hq, const float *k, int32_t ldk,
+                                 const float *v, int32_t ldv, const int32_t *pos,
+                                 const tern_rope_plan *rope, const tern_paged_batch *batch,
+                                 const tern_paged_cache *cache, float *q_out, int32_t ldqo,
+                                 int32_t *d_invalid, void *stream);
+
+/*
+ * The cache's values of a batch's rows (the inverse of the append, for tests
+ * and for handing a prefix on): k_out and v_out, device fp32 rows of Hkv heads
+ * of D (strides ldk, ldv, as in tern_kv_append_paged), get code * scale of the
+ * rows' tokens; tokens without a valid page read as 0 and are counted, once a
+ * row, in d_invalid (may be NULL).  Errors as tern_kv_append_paged.
+ */
+tern_status tern_kv_read_paged(const tern_paged_batch *batch, const tern_paged_cache *cache, float *k_out,
+                               int32_t ldk, float *v_out, int32_t ldv, int32_t *d_invalid, void *stream);
+
+/* Workspace bytes of tern_attention_paged for Hq query heads on the current
+ * device: enough for every batch and context. */
+tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_cache *cache, size_t *bytes);
+
+/*
+ * Attention of a batch's rows over the paged cache, from one row a sequence
+ * (decode) over a few drafted tokens (verify) to whole prompts (prefill).  The
+ * row of token i and query head h reads KV head h * Hkv / Hq:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j  over the tokens j <= i with
+ *   window == 0, or j > i - window (the token itself and the window - 1 before
+ *   it), or j < sinks (first tokens that stay visible),
+ * with k_j, v_j the cache's values (the rows' own tokens appended before).
+ * Tokens whose page entry lies outside [0, n_pages) or past pages_ld are
+ * treated as masked (entries of pages that a window has left may be -1); pages
+ * none of whose tokens any row sees are not read.  A row that sees no token
+ * gives 0.
+ *  q: device fp32 rows of Hq heads of D, Hq a multiple of Hkv; out likewise;
+ *  16-byte aligned, strides multiples of 4; out must not overlap q.
+ *  scale: finite.  window, sinks >= 0 (sinks is ignored without a window).
+ *  workspace: device, 16-byte aligned, at least
+ *  tern_attention_paged_workspace_bytes() bytes, no initial contents needed;
+ *  calls that may overlap need separate ones.
+ * Sums and softmax statistics are held in fp32, and the order of every sum is
+ * fixed by the lengths: the same inputs give the same bits.  T = 0 does
+ * nothing.  Errors: TERN_EINVAL for a bad batch or cache, bad shapes, strides,
+ * pointers or workspace, TERN_EUNSUPPORTED for D != 128, TERN_ECUDA.
+ */
+tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const tern_paged_batch *batch,
+                                 const tern_paged_cache *cache, int32_t window, int32_t sinks, float scale,
+                                 float *out, int32_t ldo, void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Test hook of the streamed kernels (the integer dot product and the
  * in-kernel quantisation of the Bonsai page, "Decode 为什么只能算一般"): runs
  * tern_gemv_streamed (W1 == NULL, no residual) or tern_gateup_swiglu_streamed

@@ -231,6 +231,158 @@ tern_status tern_attention_decode_q4_0(const float *q, int32_t Hq, const tern_kv
     return cuda_status(e, name);
 }
 
+// ---------------------------------------------------------------- rotary embedding, paged KV cache
+static tern_status check_rope(const tern_rope_plan *R, int32_t D, const char *name) {
+    if (!R || R->reserved != 0 || (R->flags & ~(TERN_ROPE_INTERLEAVED | TERN_ROPE_INVERSE)))
+        return fail(TERN_EINVAL, "%s: bad rotary plan (null, unknown flags or reserved != 0)", name);
+    if (!R->table || !aligned(R->table, 16) || R->n_pos < 1)
+        return fail(TERN_EINVAL, "%s: the rotary table must be 16-byte aligned with n_pos >= 1", name);
+    if (R->rot_dim < 8 || R->rot_dim % 8 != 0 || R->rot_dim > D)
+        return fail(TERN_EINVAL, "%s: rot_dim must be a multiple of 8 in 8..D", name);
+    if (R->axes < 1 || R->axes > 3) return fail(TERN_EINVAL, "%s: axes must be 1..3", name);
+    int64_t sum = 0;
+    for (int a = 0; a < 3; ++a) {
+        if (R->section[a] < 0 || (a >= R->axes && R->section[a] != 0))
+            return fail(TERN_EINVAL, "%s: sections must be >= 0, and 0 for unused axes", name);
+        sum += R->section[a];
+    }
+    if (sum != R->rot_dim / 2) return fail(TERN_EINVAL, "%s: the sections must sum to rot_dim / 2", name);
+    return TERN_OK;
+}
+
+static tern_status check_paged_cache(const tern_paged_cache *C, const char *name) {
+    if (!C || C->reserved != 0 || (C->kind != TERN_KV_INT8 && C->kind != TERN_KV_E4M3))
+        return fail(TERN_EINVAL, "%s: bad paged cache (null, unknown kind or reserved != 0)", name);
+    if (C->Hkv < 1 || C->n_pages < 1 || C->page_size < TERN_KV_BLOCK || C->page_size > 4096 ||
+        C->page_size % TERN_KV_BLOCK != 0)
+        return fail(TERN_EINVAL, "%s: Hkv, n_pages >= 1 and page_size a multiple of 16 in 16..4096 are needed", name);
+    if (C->D != 128) return fail(TERN_EUNSUPPORTED, "%s: this build takes head dimension 128", name);
+    // a row of the head dimension per (page, head, slot) is one coordinate of the kernels' copies
+    if (static_cast<int64_t>(C->n_pages) * C->Hkv > 2147483647LL / C->page_size)
+        return fail(TERN_EUNSUPPORTED, "%s: n_pages * Hkv * page_size must stay below 2^31", name);
+    if (!C->k_codes || !C->v_codes || !aligned(C->k_codes, 16) || !aligned(C->v_codes, 16) || !C->k_scales ||
+        !C->v_scales || !aligned(C->k_scales, 4) || !aligned(C->v_scales, 4))
+        return fail(TERN_EINVAL, "%s: cache arrays missing or misaligned", name);
+    return TERN_OK;
+}
+
+static tern_status check_batch(const tern_paged_batch *B, const char *name) {
+    if (!B || B->reserved != 0) return fail(TERN_EINVAL, "%s: null batch or reserved != 0", name);
+    if (B->B < 1 || B->B > 4096 || B->T < 0 || B->max_rows < 1 || B->max_ctx < 1 || B->pages_ld < 1)
+        return fail(TERN_EINVAL, "%s: B must be in 1..4096, T >= 0, max_rows, max_ctx and pages_ld >= 1", name);
+    if (!B->row_start || !B->ctx || !B->pages || !aligned(B->row_start, 4) || !aligned(B->ctx, 4) ||
+        !aligned(B->pages, 4))
+        return fail(TERN_EINVAL, "%s: row_start, ctx and pages are required (4-byte aligned)", name);
+    return TERN_OK;
+}
+
+// Rows of H heads of D floats.
+static bool good_rows(const void *p, int64_t ld, int64_t H, int64_t D) {
+    return p && aligned(p, 16) && ld % 4 == 0 && H * D <= ld;
+}
+
+tern_status tern_rope_table(double theta, double scale, int32_t rot_dim, int32_t n_pos, float *table, void *stream) {
+    const char *name = "tern_rope_table";
+    if (!(theta > 0.0) || !(scale > 0.0) || theta > 1e300 || scale > 1e300)
+        return fail(TERN_EINVAL, "%s: theta and scale must be positive and finite", name);
+    if (rot_dim < 8 || rot_dim % 8 != 0 || rot_dim > 512 || n_pos < 1)
+        return fail(TERN_EINVAL, "%s: rot_dim must be a multiple of 8 in 8..512, n_pos >= 1", name);
+    if (!table || !aligned(table, 16)) return fail(TERN_EINVAL, "%s: bad table", name);
+    return cuda_status(tern::launch_rope_table(theta, scale, rot_dim, n_pos, table, static_cast<cudaStream_t>(stream)),
+                       name);
+}
+
+tern_status tern_rope(const tern_rope_plan *rope, const int32_t *pos, int32_t T, int32_t H, int32_t D, const float *x,
+                      int32_t ldx, float *y, int32_t ldy, int32_t *d_invalid, void *stream) {
+    const char *name = "tern_rope";
+    if (T < 0 || H < 1 || D < 8 || D % 8 != 0 || D > 512)
+        return fail(TERN_EINVAL, "%s: T >= 0, H >= 1 and D a multiple of 8 in 8..512 are needed", name);
+    tern_status st = check_rope(rope, D, name);
+    if (st != TERN_OK || T == 0) return st;
+    if (!pos || !aligned(pos, 4)) return fail(TERN_EINVAL, "%s: bad pos", name);
+    if (!good_rows(x, ldx, H, D) || !good_rows(y, ldy, H, D) || (x == y && ldx != ldy))
+        return fail(TERN_EINVAL, "%s: x and y must be 16-byte aligned with strides >= H * D, multiples of 4", name);
+    if (!aligned(d_invalid, 4)) return fail(TERN_EINVAL, "%s: bad d_invalid", name);
+    return cuda_status(tern::launch_rope(*rope, pos, T, H, D, x, ldx, y, ldy, d_invalid,
+                                         static_cast<cudaStream_t>(stream)),
+                       name);
+}
+
+tern_status tern_kv_append_paged(const float *q, int32_t ldq, int32_t Hq, const float *k, int32_t ldk, const float *v,
+                                 int32_t ldv, const int32_t *pos, const tern_rope_plan *rope,
+                                 const tern_paged_batch *batch, const tern_paged_cache *cache, float *q_out,
+                                 int32_t ldqo, int32_t *d_invalid, void *stream) {
+    const char *name = "tern_kv_append_paged";
+    tern_status st = check_paged_cache(cache, name);
+    if (st == TERN_OK) st = check_batch(batch, name);
+    if (st == TERN_OK) st = check_rope(rope, cache->D, name);
+    if (st != TERN_OK || batch->T == 0) return st;
+    if (Hq < 1 || !good_rows(q, ldq, Hq, 128) || !good_rows(q_out, ldqo, Hq, 128) || (q == q_out && ldq != ldqo))
+        return fail(TERN_EINVAL, "%s: q and q_out must be 16-byte aligned with strides >= Hq * D, multiples of 4", name);
+    if (!good_rows(k, ldk, cache->Hkv, 128) || !good_rows(v, ldv, cache->Hkv, 128))
+        return fail(TERN_EINVAL, "%s: k and v must be 16-byte aligned with strides >= Hkv * D, multiples of 4", name);
+    if (!pos || !aligned(pos, 4) || !aligned(d_invalid, 4)) return fail(TERN_EINVAL, "%s: bad pos or d_invalid", name);
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return cuda_status(e, name);
+    tern::AppendLaunch A = {q,     k,      v,      ldq,   ldk, ldv, Hq, pos,
+                            *rope, *batch, *cache, q_out, ldqo, d_invalid};
+    return cuda_status(tern::launch_kv_append_paged(A, sms, static_cast<cudaStream_t>(stream)), name);
+}
+
+tern_status tern_kv_read_paged(const tern_paged_batch *batch, const tern_paged_cache *cache, float *k_out, int32_t ldk,
+                               float *v_out, int32_t ldv, int32_t *d_invalid, void *stream) {
+    const char *name = "tern_kv_read_paged";
+    tern_status st = check_paged_cache(cache, name);
+    if (st == TERN_OK) st = check_batch(batch, name);
+    if (st != TERN_OK || batch->T == 0) return st;
+    if (!good_rows(k_out, ldk, cache->Hkv, 128) || !good_rows(v_out, ldv, cache->Hkv, 128))
+        return fail(TERN_EINVAL, "%s: k_out and v_out must be 16-byte aligned with strides >= Hkv * D, multiples of 4",
+                    name);
+    if (!aligned(d_invalid, 4)) return fail(TERN_EINVAL, "%s: bad d_invalid", name);
+    return cuda_status(tern::launch_kv_read_paged(*batch, *cache, k_out, ldk, v_out, ldv, d_invalid,
+                                                  static_cast<cudaStream_t>(stream)),
+                       name);
+}
+
+tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_cache *cache, size_t *bytes) {
+    const char *name = "tern_attention_paged_workspace_bytes";
+    tern_status st = check_paged_cache(cache, name);
+    if (st != TERN_OK) return st;
+    if (Hq < 1 || Hq % cache->Hkv != 0 || !bytes)
+        return fail(TERN_EINVAL, "%s: Hq must be a multiple of Hkv, and bytes given", name);
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return cuda_status(e, name);
+    *bytes = tern::attention_paged_workspace_bytes(Hq, cache->Hkv, sms);
+    return TERN_OK;
+}
+
+tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const tern_paged_batch *batch,
+                                 const tern_paged_cache *cache, int32_t window, int32_t sinks, float scale, float *out,
+                                 int32_t ldo, void *workspace, size_t ws_bytes, void *stream) {
+    const char *name = "tern_attention_paged";
+    tern_status st = check_paged_cache(cache, name);
+    if (st == TERN_OK) st = check_batch(batch, name);
+    if (st != TERN_OK) return st;
+    if (Hq < 1 || Hq % cache->Hkv != 0) return fail(TERN_EINVAL, "%s: Hq must be a multiple of Hkv", name);
+    if (window < 0 || sinks < 0) return fail(TERN_EINVAL, "%s: window and sinks must be >= 0", name);
+    if (!(scale > -1e30f && scale < 1e30f)) return fail(TERN_EINVAL, "%s: scale must be finite", name);
+    if (batch->T == 0) return TERN_OK;
+    if (!good_rows(q, ldq, Hq, 128) || !good_rows(out, ldo, Hq, 128) || q == out)
+        return fail(TERN_EINVAL, "%s: q and out must be 16-byte aligned with strides >= Hq * D, multiples of 4", name);
+    if (!workspace || !aligned(workspace, 16))
+        return fail(TERN_EINVAL, "%s: workspace missing or misaligned", name);
+    int sms = 0;
+    cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return cuda_status(e, name);
+    if (ws_bytes < tern::attention_paged_workspace_bytes(Hq, cache->Hkv, sms))
+        return fail(TERN_EINVAL, "%s: workspace too small", name);
+    tern::PagedAttentionLaunch A = {q,     ldq, Hq,  *batch, *cache, window, sinks,
+                                    scale, out, ldo, static_cast<float *>(workspace), sms};
+    return cuda_status(tern::launch_attention_paged(A, static_cast<cudaStream_t>(stream)), name);
+}
+
 tern_status act_quant_fwht(const void *x, int32_t x_is_fp16, int32_t M, int32_t K, int32_t ldx,
                            int32_t fwht_block, int32_t flags, int8_t *q, int32_t ldq, float *s_x,
                            void *stream) {

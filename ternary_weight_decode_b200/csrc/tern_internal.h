@@ -102,6 +102,39 @@ size_t attention_workspace_bytes(int Hq, int L, int Hkv, int num_sms);
 cudaError_t launch_attention(const float *q, int Hq, const tern_kv_cache &C, int L, float *out,
                              float *part, int num_sms, cudaStream_t s, const char **why);
 
+// ---------------------------------------------------------------- paged 8-bit KV cache
+struct AppendLaunch {
+    const float *q, *k, *v;
+    int ldq, ldk, ldv, Hq;
+    const int32_t *pos;
+    tern_rope_plan rope;
+    tern_paged_batch batch;
+    tern_paged_cache cache;
+    float *q_out;
+    int ldqo;
+    int32_t *d_invalid;
+};
+cudaError_t launch_rope_table(double theta, double scale, int rot_dim, int n_pos, float *table, cudaStream_t s);
+cudaError_t launch_rope(const tern_rope_plan &R, const int32_t *pos, int T, int H, int D, const float *x, int ldx,
+                        float *y, int ldy, int32_t *d_invalid, cudaStream_t s);
+cudaError_t launch_kv_append_paged(const AppendLaunch &A, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_read_paged(const tern_paged_batch &B, const tern_paged_cache &C, float *k_out, int ldk,
+                                 float *v_out, int ldv, int32_t *d_invalid, cudaStream_t s);
+struct PagedAttentionLaunch {
+    const float *q;
+    int ldq, Hq;
+    tern_paged_batch batch;
+    tern_paged_cache cache;
+    int window, sinks;
+    float scale;
+    float *out;
+    int ldo;
+    float *workspace;
+    int num_sms;
+};
+size_t attention_paged_workspace_bytes(int Hq, int Hkv, int num_sms);
+cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s);
+
 // ---------------------------------------------------------------- quant
 cudaError_t launch_act_quant(const void *x, bool fp16, int M, int K, int ldx, int fwht_block,
                              int flags, int8_t *q, int ldq, float *s_x, cudaStream_t s);

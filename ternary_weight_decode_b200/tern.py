@@ -24,6 +24,9 @@ TERN_MATRIX_STATIC = 1
 TERN_QUANT_RMSNORM = 1
 TERN_QUANT_FWHT128 = 2
 GROUP = 128
+TERN_ROPE_INTERLEAVED, TERN_ROPE_INVERSE = 1, 2
+TERN_KV_INT8, TERN_KV_E4M3 = 0, 1
+TERN_KV_BLOCK = 16
 
 
 class TernError(RuntimeError):
@@ -57,6 +60,47 @@ class tern_kv_cache(ctypes.Structure):
         ("k_scales", ctypes.c_void_p),
         ("v_codes", ctypes.c_void_p),
         ("v_scales", ctypes.c_void_p),
+    ]
+
+
+class tern_rope_plan(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("n_pos", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("section", ctypes.c_int32 * 3),
+        ("flags", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class tern_paged_cache(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("k_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+    ]
+
+
+class tern_paged_batch(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("max_ctx", ctypes.c_int32),
+        ("row_start", ctypes.c_void_p),
+        ("ctx", ctypes.c_void_p),
+        ("pages", ctypes.c_void_p),
+        ("pages_ld", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -112,6 +156,13 @@ def lib() -> ctypes.CDLL:
                                                                   ctypes.POINTER(sz)]),
                 "tern_attention_decode_q4_0": (ctypes.c_int, [p, i32, ctypes.POINTER(tern_kv_cache), i32, p,
                                                               p, sz, p]),
+                "tern_rope_table": (ctypes.c_int, [ctypes.c_double, ctypes.c_double, i32, i32, p, p]),
+                "tern_rope": (ctypes.c_int, [p, p, i32, i32, i32, p, i32, p, i32, p, p]),
+                "tern_kv_append_paged": (ctypes.c_int, [p, i32, i32, p, i32, p, i32, p, p, p, p, p, i32, p, p]),
+                "tern_kv_read_paged": (ctypes.c_int, [p, p, p, i32, p, i32, p, p]),
+                "tern_attention_paged_workspace_bytes": (ctypes.c_int, [i32, p, ctypes.POINTER(sz)]),
+                "tern_attention_paged": (ctypes.c_int, [p, i32, i32, p, p, i32, i32, ctypes.c_float, p, i32, p,
+                                                        sz, p]),
                 "tern_gemv_fused": (ctypes.c_int, [pm, p, i32, p, i32, i32, i32, p, p, i32, p, i32, p]),
                 "tern_gateup_swiglu_fused": (ctypes.c_int, [pm, pm, p, i32, p, i32, i32, i32, p, i32,
                                                             p, i32, p]),
@@ -507,6 +558,192 @@ def tern_attention_decode_q4_0(q: torch.Tensor, cache: KVCache, L: int, out: tor
     _check(lib().tern_attention_decode_q4_0(_ptr(q), Hq, ctypes.byref(c), L, _ptr(out), _ptr(workspace),
                                             workspace.numel() * workspace.element_size(),
                                             _stream(stream)), "tern_attention_decode_q4_0")
+
+
+# ------------------------------------------------------------------ rotary embedding, paged KV cache
+def _here(*tensors) -> None:
+    """The call runs on the current device: every buffer has to be there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError(f"a buffer is on {t.device}, the current device is cuda:{cur}")
+
+
+def _heads(t: torch.Tensor, D: int | None = None) -> int:
+    """The row stride of fp32 rows of heads, a tensor or view [T, H, D]."""
+    assert t.dtype == torch.float32 and t.dim() == 3 and (D is None or t.shape[2] == D)
+    T, H, d = t.shape
+    assert (t.stride(2) == 1 or d == 1) and (t.stride(1) == d or H == 1), "heads of a row must be contiguous"
+    return t.stride(0) if T > 1 else max(H * d, 1)
+
+
+def _i32(t: torch.Tensor, *shape) -> torch.Tensor:
+    assert t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape, (tuple(t.shape), shape)
+    return t
+
+
+@dataclass
+class RopePlan:
+    """A rotary embedding: `table` fp32 [n_pos, rot_dim/2, 2] of (cos, sin), and
+    the pairs that each position axis turns (one axis, all pairs, by default)."""
+    table: torch.Tensor
+    sections: tuple | list | None = None
+    interleaved: bool = False
+    inverse: bool = False
+
+    @property
+    def axes(self) -> int:
+        return 1 if self.sections is None else len(self.sections)
+
+    @staticmethod
+    def build(theta: float, rot_dim: int, n_pos: int, sections=None, interleaved: bool = False,
+              scale: float = 1.0, device="cuda", stream=None) -> "RopePlan":
+        """The plan of the frequencies theta^(-2i/rot_dim), positions multiplied by `scale`."""
+        table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+        tern_rope_table(theta, scale, table, stream)
+        return RopePlan(table, sections, interleaved)
+
+    def struct(self) -> tern_rope_plan:
+        t = self.table
+        assert t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 3 and t.shape[2] == 2
+        sec = (t.shape[1],) if self.sections is None else tuple(self.sections)
+        assert 1 <= len(sec) <= 3
+        return tern_rope_plan(t.data_ptr(), t.shape[0], 2 * t.shape[1], len(sec),
+                              (ctypes.c_int32 * 3)(*sec, *([0] * (3 - len(sec)))),
+                              (TERN_ROPE_INTERLEAVED if self.interleaved else 0)
+                              | (TERN_ROPE_INVERSE if self.inverse else 0), 0)
+
+
+def tern_rope_table(theta: float, scale: float, table: torch.Tensor, stream=None):
+    """Fills table fp32 [n_pos, rot_dim/2, 2] with the cosines and sines of the rotary angles."""
+    assert table.dtype == torch.float32 and table.is_contiguous() and table.dim() == 3 and table.shape[2] == 2
+    _here(table)
+    _check(lib().tern_rope_table(theta, scale, 2 * table.shape[1], table.shape[0], _ptr(table), _stream(stream)),
+           "tern_rope_table")
+
+
+def tern_rope(rope: RopePlan, pos: torch.Tensor, x: torch.Tensor, y: torch.Tensor, d_invalid=None, stream=None):
+    """y [T, H, D] = x rotated by pos int32 [axes, T]; y may be x."""
+    T, H, D = x.shape
+    assert y.shape == x.shape
+    _i32(pos, rope.axes, T)
+    _here(rope.table, pos, x, y, d_invalid)
+    r = rope.struct()
+    _check(lib().tern_rope(ctypes.addressof(r), pos.data_ptr(), T, H, D, x.data_ptr(), _heads(x), y.data_ptr(),
+                           _heads(y), _ptr(d_invalid), _stream(stream)), "tern_rope")
+
+
+@dataclass
+class PagedCache:
+    """A paged 8-bit KV cache of one layer: codes uint8 [n_pages, Hkv, page_size, D]
+    and fp32 scales [n_pages, Hkv, page_size/16] for K and for V."""
+    kind: int
+    Hkv: int
+    D: int
+    page_size: int
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+    @staticmethod
+    def empty(kind: int, Hkv: int, D: int, page_size: int, n_pages: int, device="cuda") -> "PagedCache":
+        def codes():
+            return torch.zeros((n_pages, Hkv, page_size, D), dtype=torch.uint8, device=device)
+
+        def scales():
+            return torch.zeros((n_pages, Hkv, page_size // TERN_KV_BLOCK), dtype=torch.float32, device=device)
+        return PagedCache(kind, Hkv, D, page_size, codes(), scales(), codes(), scales())
+
+    def struct(self) -> tern_paged_cache:
+        n = self.k_codes.shape[0]
+        for codes, scales in ((self.k_codes, self.k_scales), (self.v_codes, self.v_scales)):
+            assert codes.dtype == torch.uint8 and codes.is_contiguous() and scales.is_contiguous()
+            assert scales.dtype == torch.float32 and tuple(codes.shape) == (n, self.Hkv, self.page_size, self.D)
+            assert tuple(scales.shape) == (n, self.Hkv, self.page_size // TERN_KV_BLOCK)
+        return tern_paged_cache(self.kind, self.Hkv, self.D, self.page_size, n, 0, self.k_codes.data_ptr(),
+                                self.k_scales.data_ptr(), self.v_codes.data_ptr(), self.v_scales.data_ptr())
+
+
+@dataclass
+class PagedBatch:
+    """A batch over a paged cache (include/tern.h): row_start int32 [B + 1], ctx
+    int32 [B], pages int32 [B, pages_ld], all on the device; T rows, at most
+    about max_rows rows and max_ctx tokens a sequence."""
+    row_start: torch.Tensor
+    ctx: torch.Tensor
+    pages: torch.Tensor
+    T: int
+    max_rows: int
+    max_ctx: int
+
+    def struct(self) -> tern_paged_batch:
+        B = self.ctx.shape[0]
+        _i32(self.row_start, B + 1)
+        _i32(self.ctx, B)
+        _i32(self.pages, B, self.pages.shape[1])
+        return tern_paged_batch(B, self.T, self.max_rows, self.max_ctx, self.row_start.data_ptr(),
+                                self.ctx.data_ptr(), self.pages.data_ptr(), self.pages.shape[1], 0)
+
+    def here(self, cache: PagedCache, *tensors) -> None:
+        _here(self.row_start, self.ctx, self.pages, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales,
+              *tensors)
+
+
+def tern_kv_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, rope: RopePlan,
+                         batch: PagedBatch, cache: PagedCache, q_out: torch.Tensor, d_invalid=None, stream=None):
+    """q_out [T, Hq, D] = q rotated; k (rotated) and v [T, Hkv, D] quantised into the cache.
+    pos int32 [axes, T]; q_out may be q."""
+    T, Hq, D = q.shape
+    assert q_out.shape == q.shape and T == batch.T and D == cache.D
+    assert tuple(k.shape) == (T, cache.Hkv, D) and v.shape == k.shape
+    _i32(pos, rope.axes, T)
+    batch.here(cache, rope.table, pos, q, k, v, q_out, d_invalid)
+    r, b, c = rope.struct(), batch.struct(), cache.struct()
+    _check(lib().tern_kv_append_paged(q.data_ptr(), _heads(q), Hq, k.data_ptr(), _heads(k), v.data_ptr(), _heads(v),
+                                      pos.data_ptr(), ctypes.addressof(r), ctypes.addressof(b), ctypes.addressof(c),
+                                      q_out.data_ptr(), _heads(q_out), _ptr(d_invalid), _stream(stream)),
+           "tern_kv_append_paged")
+
+
+def tern_kv_read_paged(batch: PagedBatch, cache: PagedCache, k_out: torch.Tensor, v_out: torch.Tensor,
+                       d_invalid=None, stream=None):
+    """k_out, v_out [T, Hkv, D] = the cache's values of the batch's rows."""
+    assert tuple(k_out.shape) == (batch.T, cache.Hkv, cache.D) and v_out.shape == k_out.shape
+    batch.here(cache, k_out, v_out, d_invalid)
+    b, c = batch.struct(), cache.struct()
+    _check(lib().tern_kv_read_paged(ctypes.addressof(b), ctypes.addressof(c), k_out.data_ptr(), _heads(k_out),
+                                    v_out.data_ptr(), _heads(v_out), _ptr(d_invalid), _stream(stream)),
+           "tern_kv_read_paged")
+
+
+def tern_attention_paged_workspace_bytes(Hq: int, cache: PagedCache) -> int:
+    b = ctypes.c_size_t()
+    c = cache.struct()
+    _check(lib().tern_attention_paged_workspace_bytes(Hq, ctypes.addressof(c), ctypes.byref(b)),
+           "tern_attention_paged_workspace_bytes")
+    return b.value
+
+
+def attention_paged_workspace(Hq: int, cache: PagedCache) -> torch.Tensor:
+    """A workspace for tern_attention_paged: one serves every batch of calls that do not overlap."""
+    n = tern_attention_paged_workspace_bytes(Hq, cache)
+    return torch.empty(((n + 15) // 16) * 4, dtype=torch.float32, device=cache.k_codes.device)
+
+
+def tern_attention_paged(q: torch.Tensor, batch: PagedBatch, cache: PagedCache, out: torch.Tensor,
+                         workspace: torch.Tensor, window: int = 0, sinks: int = 0, scale: float | None = None,
+                         stream=None):
+    """out [T, Hq, D] = causal attention of the batch's rows q over the cache;
+    window tokens (0: all) and the first `sinks` are visible; scale 1/sqrt(D) by default."""
+    T, Hq, D = q.shape
+    assert out.shape == q.shape and T == batch.T and D == cache.D
+    batch.here(cache, q, out, workspace)
+    b, c = batch.struct(), cache.struct()
+    _check(lib().tern_attention_paged(q.data_ptr(), _heads(q), Hq, ctypes.addressof(b), ctypes.addressof(c), window,
+                                      sinks, D ** -0.5 if scale is None else scale, out.data_ptr(), _heads(out),
+                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                      _stream(stream)), "tern_attention_paged")
 
 
 ENGINE_TENSOR_CORES, ENGINE_CUDA_CORES = 0, 1
