@@ -629,8 +629,9 @@ tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_ca
  *  16-byte aligned, strides multiples of 4; out must not overlap q.
  *  scale: finite.  window, sinks >= 0 (sinks is ignored without a window).
  *  workspace: device, 16-byte aligned, at least
- *  tern_attention_paged_workspace_bytes() bytes, no initial contents needed;
- *  calls that may overlap need separate ones.
+ *  tern_attention_paged_workspace_bytes() bytes, its first 4096 bytes all zero
+ *  before its first use (counters, zero again after every call); calls that
+ *  may overlap need separate ones.
  * Sums and softmax statistics are held in fp32, and the order of every sum is
  * fixed by the lengths: the same inputs give the same bits.  T = 0 does
  * nothing.  Errors: TERN_EINVAL for a bad batch or cache, bad shapes, strides,

@@ -380,7 +380,10 @@ tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const 
         return fail(TERN_EINVAL, "%s: workspace too small", name);
     tern::PagedAttentionLaunch A = {q,     ldq, Hq,  *batch, *cache, window, sinks,
                                     scale, out, ldo, static_cast<float *>(workspace), sms};
-    return cuda_status(tern::launch_attention_paged(A, static_cast<cudaStream_t>(stream)), name);
+    const char *why = nullptr;
+    e = tern::launch_attention_paged(A, static_cast<cudaStream_t>(stream), &why);
+    if (why) return fail(TERN_EUNSUPPORTED, "tern_attention_paged: %s", why);
+    return cuda_status(e, name);
 }
 
 tern_status act_quant_fwht(const void *x, int32_t x_is_fp16, int32_t M, int32_t K, int32_t ldx,

@@ -133,7 +133,7 @@ struct PagedAttentionLaunch {
     int num_sms;
 };
 size_t attention_paged_workspace_bytes(int Hq, int Hkv, int num_sms);
-cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s);
+cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s, const char **why);
 
 // ---------------------------------------------------------------- quant
 cudaError_t launch_act_quant(const void *x, bool fp16, int M, int K, int ldx, int fwht_block,

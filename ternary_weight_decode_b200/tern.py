@@ -726,9 +726,10 @@ def tern_attention_paged_workspace_bytes(Hq: int, cache: PagedCache) -> int:
 
 
 def attention_paged_workspace(Hq: int, cache: PagedCache) -> torch.Tensor:
-    """A workspace for tern_attention_paged: one serves every batch of calls that do not overlap."""
+    """A workspace for tern_attention_paged (zeroed; its counters are zero again after every
+    call): one serves every batch of calls that do not overlap."""
     n = tern_attention_paged_workspace_bytes(Hq, cache)
-    return torch.empty(((n + 15) // 16) * 4, dtype=torch.float32, device=cache.k_codes.device)
+    return torch.zeros(((n + 15) // 16) * 4, dtype=torch.float32, device=cache.k_codes.device)
 
 
 def tern_attention_paged(q: torch.Tensor, batch: PagedBatch, cache: PagedCache, out: torch.Tensor,
