@@ -8,23 +8,25 @@
 // tokens times the query heads of the group) are taken eight at a time: an
 // item.  An item's work is its visible tiles of 16 tokens (one scale block
 // each).  All tiles of all items form one line, cut into equal ranges, one per
-// CTA, so that uneven contexts fill the GPU evenly; the lengths are read on the
-// device.  An item cut by a range's end leaves partial results (m, z and the
-// unnormalised sum) in the workspace; the CTA that finishes its last part
-// merges them in the order of the ranges, so the result does not depend on
+// warp of the grid, so that uneven contexts fill the GPU evenly; the lengths
+// are read on the device.  A warp walks its range without waiting for others:
+// the ring of TMA stages runs on across items.  An item that lies inside one
+// warp's range is written out by it; the pieces of the others (m, z and the
+// unnormalised sum) are merged in the order of the ranges, first those of a
+// CTA through shared memory, then those of several CTAs through the workspace,
+// by the CTA that finishes the last of them, so the result does not depend on
 // timing.
 //
-// A warp takes every kWarps-th tile of its CTA's part of an item: TMA brings
-// the 16 key and 16 value rows (2 KB each, 128-byte swizzle) into the warp's
-// own ring of stages, and the warp multiplies on the tensor cores with fp16
-// operands and fp32 accumulators (m16n8k16).  Codes of 8 bits are exact in
-// fp16.  Queries and softmax weights are fp32 values, held as two fp16 parts
-// hi + lo (22 bits, the query row first scaled by a power of two): the eight
-// rows' hi parts fill rows 0-7 of the 16-row operand and their lo parts rows
-// 8-15, so the second part costs no further matrix instruction, and the two
-// halves of a result lie in one thread.  The value product of each tile starts
-// from zero and is added to the fp32 sum with the block's scale, so that no
-// long chain of sums runs inside the tensor cores.
+// TMA brings the 16 key and 16 value rows of a tile (2 KB each, 128-byte
+// swizzle) into the warp's own stages, and the warp multiplies on the tensor
+// cores with fp16 operands and fp32 accumulators (m16n8k16).  Codes of 8 bits
+// are exact in fp16.  Queries and softmax weights are fp32 values, held as two
+// fp16 parts hi + lo (22 bits, the query row first scaled by a power of two):
+// the eight rows' hi parts fill rows 0-7 of the 16-row operand and their lo
+// parts rows 8-15, so the second part costs no further matrix instruction, and
+// the two halves of a result lie in one thread.  The value product of each
+// tile starts from zero and is added to the fp32 sum with the block's scale,
+// so that no long chain of sums runs inside the tensor cores.
 //
 // The order of the 128 dimensions inside a score's sum is free: lane (g, t)
 // (g = lane / 4, t = lane % 4) feeds bytes 32t .. 32t+31 of key g, two 16-byte
@@ -40,9 +42,8 @@ namespace tern {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 4;
 constexpr int kRows = 8;         // rows of an item
 constexpr int kStages = 3;       // tiles in flight per warp
 constexpr int kTileBytes = kPB * kPD;       // 2048: one block's codes of K or of V
@@ -164,187 +165,274 @@ struct State {
     float o[16][2];
 };
 
+// Quotient of nonnegative numbers; 64-bit division is a long routine that
+// nearly every call can do without.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// The line of `total` tiles in n ranges: the first `more` hold base + 1 tiles,
+// the others base (n <= total, so none is empty).
+struct Ranges {
+    long long base, more;
+    __device__ __forceinline__ long long begin(int i) const { return base * i + min(static_cast<long long>(i), more); }
+    __device__ __forceinline__ int owner(long long u) const {
+        const long long big = more * (base + 1);
+        return static_cast<int>(u < big ? quot(u, base + 1) : more + quot(u - big, base));
+    }
+};
+
+// A place on the line: tile k of an item.
+struct Cursor {
+    int b, head, rt, k;
+    Seq s;
+    Tiles tl;
+    __device__ __forceinline__ int units() const { return max(1, tl.n); }
+    __device__ __forceinline__ int tile() const { return k < tl.sink ? k : tl.lo + k - tl.sink; }
+};
+
+__device__ __forceinline__ void advance(const AttnParams &p, Cursor &x, int n) {
+    x.k += n;
+    while (x.k >= x.units()) {
+        x.k -= x.units();
+        if ((x.rt + 1) * kRows < x.s.rows) {
+            ++x.rt;
+        } else {
+            x.rt = 0;
+            if (++x.head == p.v.Hkv) {
+                x.head = 0;
+                do {
+                    if (++x.b >= p.v.B) return;  // past the line: the caller counts its tiles
+                    x.s = sequence(p, x.b);
+                } while (x.s.rows == 0);
+            }
+        }
+        x.tl = tiles_of(p, x.s, x.rt);
+    }
+}
+
+// What a warp's walk needs of one tile.
+struct __align__(16) TileInfo {
+    int bi;          // scale block of K and V (its 16 rows begin at 16 bi), -1: none
+    float ks, vs;
+    int j0;          // first token
+    int b, head, rt; // item
+    int k;           // tile of the item, times 2, + 1 for the item's last tile
+};
+
+// A piece of a cut item.
+struct Piece {
+    int valid, ends;   // ends: holds the item's last tile
+    int b, head, rt, units;
+    long long u0;      // line index of the item's first tile
+};
+
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kPieceFloats = kRows * kPD;
+struct SplitShared {
+    float first[kWarps][kPieceFloats];  // the piece a warp's range begins with (its last piece lies in its ring)
+    TileInfo info[kWarps][2][32];
+    float m[kWarps][2][kRows], z[kWarps][2][kRows];
+    Piece piece[kWarps][2];
+    uint64_t bars[kWarps][kStages];
+    long long chunk[kThreads];          // line index where each thread's sequences begin
+    long long scan[kWarps];
+    int last[2];
+};
+constexpr size_t kSplitSmem = kRingBytes + sizeof(SplitShared) + 1024;
+static_assert(kSplitSmem <= 227 * 1024, "shared memory of one CTA");
+
+// Row rr of an item to its place in out: four dimensions a lane.
+__device__ __forceinline__ void write_row(const AttnParams &p, int start, int head, int row, float4 o, float z, int d) {
+    const float iz = z > 0.0f ? 1.0f / z : 0.0f;
+    *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(start + row / p.GQ) * p.ldo +
+                                (head * p.GQ + row % p.GQ) * kPD + d) =
+        make_float4(o.x * iz, o.y * iz, o.z * iz, o.w * iz);
+}
+
+__device__ __forceinline__ void add_scaled(float4 &o, float &z, float f, float4 x, float xz) {
+    z = fmaf(f, xz, z);
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+}
+
 template <int KIND>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_split_paged_kernel(AttnParams p, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap) {
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ uint64_t bars[kWarps][kStages];
-    __shared__ long long scan[kWarps];
-    __shared__ long long s_total, s_off;
-    __shared__ int s_b, s_last;
-    __shared__ float wm[kWarps][kRows], wz[kWarps][kRows];
+    extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *merge = reinterpret_cast<float *>(ring);  // [kWarps][kRows][kPD], between segments
+    SplitShared &S = *reinterpret_cast<SplitShared *>(ring + kRingBytes);
     const PagedView &v = p.v;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int c = blockIdx.x;
+    uint8_t *my_ring = ring + warp * kStages * kStageBytes;
 
     if (tid == 0) {
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
-        for (int w = 0; w < kWarps; ++w)
-            for (int s = 0; s < kStages; ++s) mbar_init(&bars[w][s], 1);
+    }
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(&S.bars[warp][s], 1);
         fence_mbar_init();
+        S.piece[warp][0].valid = S.piece[warp][1].valid = 0;
     }
     pdl_wait();
 
-    // ---- this CTA's range of the line of tiles
+    // ---- the line's length, and where each thread's sequences begin on it
     const int per = (v.B + kThreads - 1) / kThreads;
-    const int b0 = tid * per, b1 = min(v.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += v.Hkv * head_units(p, sequence(p, b));
+    for (int b = tid * per; b < min(v.B, tid * per + per); ++b) mine += v.Hkv * head_units(p, sequence(p, b));
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
-    if (lane == 31) scan[warp] = incl;
+    if (lane == 31) S.scan[warp] = incl;
     __syncthreads();
-    long long before = 0, total = 0;
+    long long total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
+        if (w < warp) before += S.scan[w];
+        total += S.scan[w];
     }
-    const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // no range is empty
-    long long u = c < G ? total * c / G : 0;
-    const long long u_end = c < G ? total * (c + 1) / G : 0;
-    {
-        const long long base = before + incl - mine;
-        if (c < G && u >= base && u < base + mine) {
-            long long off = u - base;
-            int b = b0;
-            for (; b < b1; ++b) {
-                const long long n = v.Hkv * head_units(p, sequence(p, b));
-                if (off < n) break;
-                off -= n;
-            }
-            s_b = b;
-            s_off = off;
-        }
-    }
+    S.chunk[tid] = before + incl - mine;
     __syncthreads();
+    const int nw = static_cast<int>(min(static_cast<long long>(gridDim.x) * kWarps, total));
+    Ranges R = {0, 0};
+    if (total > 0) {
+        R.base = quot(total, nw);
+        R.more = total - R.base * nw;
+    }
+    const int wi = c * kWarps + warp;  // this warp's range
+    const long long u0 = wi < nw ? R.begin(wi) : 0;
+    const int count = wi < nw ? static_cast<int>(R.begin(wi + 1) - u0) : 0;
 
-    uint32_t phases = 0;  // parity of each of this warp's stages
-    uint8_t *my_ring = ring + warp * kStages * kStageBytes;
-    int b = u < u_end ? s_b : 0;
-    long long off = u < u_end ? s_off : 0;
-
-    while (u < u_end) {
-        // ---- the segment: tiles [k0, k1) of item (b, head, rt)
-        const Seq s = sequence(p, b);
-        const long long per_head = head_units(p, s);
-        if (off >= per_head * v.Hkv) {  // the next sequence
-            off -= per_head * v.Hkv;
-            ++b;
-            continue;
-        }
-        const int head = static_cast<int>(off / per_head);
-        long long rem = off - head * per_head;
-        int rt = 0;
-        Tiles tl = tiles_of(p, s, 0);
-        while (rem >= max(1, tl.n)) {
-            rem -= max(1, tl.n);
-            tl = tiles_of(p, s, ++rt);
-        }
-        const int item_units = max(1, tl.n);
-        const int k0 = static_cast<int>(rem);
-        const int k1 = static_cast<int>(min(static_cast<long long>(item_units), rem + (u_end - u)));
-        const long long item_u0 = u - k0;
-
-        // ---- queries: row g of the item, dimensions 32 t .. 32 t + 31
-        const int r = kRows * rt + g;
-        const bool row_ok = r < s.rows;
-        const int pos = s.first + (row_ok ? r / p.GQ : 0);
-        uint32_t qhi[8][2], qlo[8][2];
-        float rowf;
+    if (count > 0) {
+        // ---- the range's first tile
+        Cursor cur;
         {
-            const float *qp = p.q + static_cast<int64_t>(s.start + r / p.GQ) * p.ldq +
-                              (head * p.GQ + r % p.GQ) * kPD + 32 * t;
-            float4 x[8];
-            float amax = 0.0f;
+            int lo = 0;  // the last thread whose sequences begin at or before u0: 12 probes a lane, one ballot each
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = row_ok ? *reinterpret_cast<const float4 *>(qp + 4 * i) : make_float4(0, 0, 0, 0);
-                amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w))));
+            for (int i = 0; i < kWarps; ++i) {
+                const unsigned le = __ballot_sync(0xffffffffu, S.chunk[32 * i + lane] <= u0);
+                if (le) lo = 32 * i + 31 - __clz(le);
             }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // the row times 2^e: its largest value in [2^7, 2^8)
-            const int e = max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23)));
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            rowf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                split2(x[i].x * up, x[i].y * up, qhi[i][0], qlo[i][0]);
-                split2(x[i].z * up, x[i].w * up, qhi[i][1], qlo[i][1]);
+            long long off = u0 - S.chunk[lo];
+            int b = lo * per;
+            long long ph;
+            for (;; ++b) {
+                cur.s = sequence(p, b);
+                ph = head_units(p, cur.s);
+                if (off < ph * v.Hkv) break;
+                off -= ph * v.Hkv;
             }
+            cur.b = b;
+            cur.head = static_cast<int>(quot(off, ph));
+            off -= cur.head * ph;
+            cur.rt = 0;
+            cur.tl = tiles_of(p, cur.s, 0);
+            while (off >= cur.units()) {
+                off -= cur.units();
+                cur.tl = tiles_of(p, cur.s, ++cur.rt);
+            }
+            cur.k = static_cast<int>(off);
         }
-
-        // ---- this warp's tiles of the segment: k0 + warp, k0 + warp + kWarps, ...
-        State st;
-        st.m = -INFINITY;
-        st.z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) st.o[i][0] = st.o[i][1] = 0.0f;
-        const int k_real = min(k1, tl.n);  // an item without tiles has no real one
-        const int count = k0 + warp < k_real ? (k_real - k0 - warp + kWarps - 1) / kWarps : 0;
-        const int p_min = s.first + kRows * rt / p.GQ, p_max = s.first + (min(kRows * rt + kRows, s.rows) - 1) / p.GQ;
-        int bi_lane = -1;             // block of tile (group of 32) + lane
-        float ks_lane = 0.0f, vs_lane = 0.0f;
-        int bi_next = -1;             // the same of the next group
-        float ks_next = 0.0f, vs_next = 0.0f;
-        auto tile_at = [&](int i) {
-            const int k = k0 + warp + i * kWarps;
-            return k < tl.sink ? k : tl.lo + k - tl.sink;
-        };
-        auto fetch = [&](int i0, int &bi, float &ks, float &vs) {
-            bi = -1;
+        // each lane keeps its own cursor, 32 tiles apart from its last: tile i of the range is in info[i / 32 % 2][i % 32]
+        if (lane < count) advance(p, cur, lane);
+        auto fill = [&](int i0) {
             if (i0 + lane < count) {
-                const int64_t x = block_index(v, b, tile_at(i0 + lane));
-                if (x >= 0) {
-                    bi = static_cast<int>(x) + head * v.bpp;
-                    ks = __ldg(v.ks + bi);
-                    vs = __ldg(v.vs + bi);
+                TileInfo x;
+                x.j0 = cur.tile() * kPB;
+                x.b = cur.b;
+                x.head = cur.head;
+                x.rt = cur.rt;
+                x.k = 2 * cur.k + (cur.k + 1 == cur.units() ? 1 : 0);
+                x.bi = -1;
+                x.ks = x.vs = 0.0f;
+                if (cur.tl.n > 0) {
+                    const int64_t bi = block_index(v, cur.b, cur.tile());
+                    if (bi >= 0) {
+                        x.bi = static_cast<int>(bi) + cur.head * v.bpp;
+                        x.ks = v.ks[x.bi];
+                        x.vs = v.vs[x.bi];
+                    }
+                }
+                S.info[warp][(i0 >> 5) & 1][lane] = x;
+                if (i0 + 32 + lane < count) advance(p, cur, 32);
+            }
+            __syncwarp();
+        };
+        auto start = [&](int i) {  // tile i's copies into its stage
+            if (lane == 0 && i < count) {
+                const int bi = S.info[warp][(i >> 5) & 1][i & 31].bi;
+                if (bi >= 0) {
+                    uint8_t *dst = my_ring + (i % kStages) * kStageBytes;
+                    uint64_t *bar = &S.bars[warp][i % kStages];
+                    mbar_arrive_expect_tx(bar, kStageBytes);
+                    tma_load_2d_nohint(dst, &kmap, 0, bi * kPB, bar);
+                    tma_load_2d_nohint(dst + kTileBytes, &vmap, 0, bi * kPB, bar);
                 }
             }
         };
-        fetch(0, bi_lane, ks_lane, vs_lane);
-        fetch(32, bi_next, ks_next, vs_next);
-        auto start = [&](int i, int bi) {
-            if (lane == 0 && bi >= 0) {
-                uint8_t *dst = my_ring + (i % kStages) * kStageBytes;
-                uint64_t *bar = &bars[warp][i % kStages];
-                mbar_arrive_expect_tx(bar, kStageBytes);
-                tma_load_2d_nohint(dst, &kmap, 0, bi * kPB, bar);
-                tma_load_2d_nohint(dst + kTileBytes, &vmap, 0, bi * kPB, bar);
-            }
-        };
-        // the merge buffer of the segment before lay where the stages are
-        fence_proxy_async_smem();
-        __syncthreads();
+        fill(0);
 #pragma unroll
-        for (int i = 0; i < kStages; ++i) start(i, __shfl_sync(0xffffffffu, bi_lane, i));
+        for (int i = 0; i < kStages; ++i) start(i);
+        fill(32);
 
+        State st;
+        uint32_t qhi[8][2], qlo[8][2];
+        Seq s = {};
+        float rowf = 0.0f;
+        int pos = 0, p_min = 0, p_max = 0, k_first = 0;
+        uint32_t phases = 0;  // parity of each stage
+        int stage = 0;
         for (int i = 0; i < count; ++i) {
-            if ((i & 31) == 0 && i > 0) {
-                bi_lane = bi_next;
-                ks_lane = ks_next;
-                vs_lane = vs_next;
-                fetch(i + 32, bi_next, ks_next, vs_next);
+            if ((i & 31) == 0 && i > 0) fill(i + 32);
+            const TileInfo x = S.info[warp][(i >> 5) & 1][i & 31];
+            if (i == 0 || (x.k >> 1) == 0) {
+                // ---- a new item: row g's query, dimensions 32 t .. 32 t + 31, as hi + lo operands
+                s = sequence(p, x.b);
+                k_first = x.k >> 1;
+                const int r = kRows * x.rt + g;
+                const bool row_ok = r < s.rows;
+                pos = s.first + (row_ok ? r / p.GQ : 0);
+                p_min = s.first + kRows * x.rt / p.GQ;
+                p_max = s.first + (min(kRows * x.rt + kRows, s.rows) - 1) / p.GQ;
+                const float *qp = p.q + static_cast<int64_t>(s.start + r / p.GQ) * p.ldq +
+                                  (x.head * p.GQ + r % p.GQ) * kPD + 32 * t;
+                float4 q4[8];
+                float amax = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    q4[e] = row_ok ? *reinterpret_cast<const float4 *>(qp + 4 * e) : make_float4(0, 0, 0, 0);
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(q4[e].x), fabsf(q4[e].y)), fmaxf(fabsf(q4[e].z), fabsf(q4[e].w))));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // the row times 2^e: its largest value in [2^7, 2^8)
+                const int e = max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23)));
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                rowf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    split2(q4[n].x * up, q4[n].y * up, qhi[n][0], qlo[n][0]);
+                    split2(q4[n].z * up, q4[n].w * up, qhi[n][1], qlo[n][1]);
+                }
+                st.m = -INFINITY;
+                st.z = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 16; ++n) st.o[n][0] = st.o[n][1] = 0.0f;
             }
-            const int bi = __shfl_sync(0xffffffffu, bi_lane, i & 31);
-            const float ks = __shfl_sync(0xffffffffu, ks_lane, i & 31);
-            const float vs = __shfl_sync(0xffffffffu, vs_lane, i & 31);
-            const int stage = i % kStages;
-            if (bi >= 0) {
-                mbar_wait_bounded(&bars[warp][stage], (phases >> stage) & 1u);
+            if (x.bi >= 0) {
+                mbar_wait_bounded(&S.bars[warp][stage], (phases >> stage) & 1u);
                 phases ^= 1u << stage;
                 const uint8_t *kt = my_ring + stage * kStageBytes, *vt = kt + kTileBytes;
-                const int tile = tile_at(i), j0 = tile * kPB;
                 // scores: tokens j0 + 2t, + 1 (n = 0) and j0 + 8 + 2t, + 1 (n = 1) of row g
                 float sc[2][4];
 #pragma unroll
@@ -365,19 +453,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         }
                     }
                 }
-                const float f = rowf * ks;
-                float x[4] = {(sc[0][0] + sc[0][2]) * f, (sc[0][1] + sc[0][3]) * f, (sc[1][0] + sc[1][2]) * f,
+                const float f = rowf * x.ks;
+                float y[4] = {(sc[0][0] + sc[0][2]) * f, (sc[0][1] + sc[0][3]) * f, (sc[1][0] + sc[1][2]) * f,
                               (sc[1][1] + sc[1][3]) * f};
-                const bool whole = j0 + kPB - 1 <= p_min &&
-                                   (p.window == 0 || j0 > p_max - p.window || j0 + kPB <= p.sinks);
+                const bool whole = x.j0 + kPB - 1 <= p_min &&
+                                   (p.window == 0 || x.j0 > p_max - p.window || x.j0 + kPB <= p.sinks);
                 if (!whole) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int j = j0 + (e >> 1) * 8 + 2 * t + (e & 1);
-                        if (j > pos || (p.window > 0 && j <= pos - p.window && j >= p.sinks)) x[e] = -INFINITY;
+                        const int j = x.j0 + (e >> 1) * 8 + 2 * t + (e & 1);
+                        if (j > pos || (p.window > 0 && j <= pos - p.window && j >= p.sinks)) y[e] = -INFINITY;
                     }
                 }
-                float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float mn = fmaxf(st.m, mx - kPScale);
@@ -394,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
                 float w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = ex2(x[e] - ref);
+                for (int e = 0; e < 4; ++e) w[e] = ex2(y[e] - ref);
                 st.z += (w[0] + w[1]) + (w[2] + w[3]);
                 uint32_t a[4];
                 split2(w[0], w[1], a[0], a[1]);
@@ -409,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     vw[k][1] = w4.y;
                     vw[k][2] = w4.z;
                     vw[k][3] = w4.w;
-                    if (j0 + kPB > s.end && j0 + rr >= s.end)  // slots behind the context hold anything
+                    if (x.j0 + kPB > s.end && x.j0 + rr >= s.end)  // slots behind the context hold anything
                         vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0;
                 }
 #pragma unroll
@@ -426,132 +514,160 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         if (e == 2) mma_f16(d, a, code_pair<KIND, 0>(xh), code_pair<KIND, 0>(yh));
                         if (e == 3) mma_f16(d, a, code_pair<KIND, 1>(xh), code_pair<KIND, 1>(yh));
                         float(&o)[2] = st.o[4 * q4 + e];
-                        o[0] = fmaf(vs, d[0] + d[2], o[0]);
-                        o[1] = fmaf(vs, d[1] + d[3], o[1]);
+                        o[0] = fmaf(x.vs, d[0] + d[2], o[0]);
+                        o[1] = fmaf(x.vs, d[1] + d[3], o[1]);
                     }
                 }
                 fence_proxy_async_smem();  // these reads before the refill of the stage
                 __syncwarp();
             }
-            const int in = i + kStages;
-            if (in < count) {
-                // tile in's block: of this group of 32, or of the next
-                const int cur = __shfl_sync(0xffffffffu, bi_lane, in & 31);
-                const int nxt = __shfl_sync(0xffffffffu, bi_next, in & 31);
-                start(in, (in >> 5) == (i >> 5) ? cur : nxt);
-            }
-        }
+            start(i + kStages);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
 
-        // ---- the warps' results, merged in warp order
-        st.z += __shfl_xor_sync(0xffffffffu, st.z, 1);
-        st.z += __shfl_xor_sync(0xffffffffu, st.z, 2);
-        __syncthreads();  // the stages are free
-        if (t == 0) {
-            wm[warp][g] = st.m;
-            wz[warp][g] = st.z;
-        }
-        {
-            float *mg = merge + (warp * kRows + g) * kPD + 32 * t;
+            const bool ends = (x.k & 1) != 0;
+            if (ends || i + 1 == count) {
+                // ---- the item, or this warp's piece of it, is done
+                st.z += __shfl_xor_sync(0xffffffffu, st.z, 1);
+                st.z += __shfl_xor_sync(0xffffffffu, st.z, 2);
+                const int r = kRows * x.rt + g;
+                if (k_first == 0 && ends) {
+                    if (r < s.rows) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                *reinterpret_cast<float4 *>(mg + i) =
-                    make_float4(st.o[i][0], st.o[i + 1][0], st.o[i + 2][0], st.o[i + 3][0]);
-                *reinterpret_cast<float4 *>(mg + 16 + i) =
-                    make_float4(st.o[i][1], st.o[i + 1][1], st.o[i + 2][1], st.o[i + 3][1]);
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int n = 0; n < 16; n += 4)
+                                write_row(p, s.start, x.head, r,
+                                          make_float4(st.o[n][e], st.o[n + 1][e], st.o[n + 2][e], st.o[n + 3][e]), st.z,
+                                          32 * t + 16 * e + n);
+                    }
+                } else {
+                    const int slot = k_first > 0 ? 0 : 1;  // a range's first piece, or its last
+                    float *dst = (slot == 0 ? S.first[warp] : reinterpret_cast<float *>(my_ring)) + g * kPD + 32 * t;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int n = 0; n < 16; n += 4)
+                            *reinterpret_cast<float4 *>(dst + 16 * e + n) =
+                                make_float4(st.o[n][e], st.o[n + 1][e], st.o[n + 2][e], st.o[n + 3][e]);
+                    if (t == 0) {
+                        S.m[warp][slot][g] = st.m;
+                        S.z[warp][slot][g] = st.z;
+                    }
+                    if (lane == 0) {
+                        Piece pc;
+                        pc.valid = 1;
+                        pc.ends = ends;
+                        pc.b = x.b;
+                        pc.head = x.head;
+                        pc.rt = x.rt;
+                        pc.u0 = u0 + i - (x.k >> 1);
+                        pc.units = max(1, tiles_of(p, s, x.rt).n);
+                        S.piece[warp][slot] = pc;
+                    }
+                }
             }
         }
-        __syncthreads();
-        const bool complete = k0 == 0 && k1 == item_units;
-        float *rec = p.part + static_cast<int64_t>(2 * c + (k0 == 0 ? 1 : 0)) * kRecFloats;
+    }
+    __syncthreads();
+
+    // ---- pieces of this CTA's warps: group a begins with a warp's last piece
+    // (a = warp) or with the first piece of warp 0 (a = -1), and goes on with
+    // the first pieces of the warps behind it until the item ends
+    bool cut[2] = {false, false};  // groups that other CTAs share: begun before this CTA, going on behind it
+    Piece shared_piece[2];
+    for (int a = -1; a < kWarps; ++a) {
+        const int w0 = max(a, 0), slot0 = a < 0 ? 0 : 1;
+        const Piece &pc = S.piece[w0][slot0];
+        if (!pc.valid) continue;
+        int w1 = w0;  // last warp of the group
+        bool ends = pc.ends;
+        while (!ends && w1 + 1 < kWarps && S.piece[w1 + 1][0].valid) ends = S.piece[++w1][0].ends;
+        const bool complete = a >= 0 && ends;
+        if (!complete) {
+            cut[slot0] = true;
+            shared_piece[slot0] = pc;
+        }
+        const Seq s = sequence(p, pc.b);
         for (int rr = warp; rr < kRows; rr += kWarps) {
-            const int row = kRows * rt + rr;
+            const int row = kRows * pc.rt + rr;
             if (row >= s.rows) break;
             float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w][rr]);
+            for (int w = w0; w <= w1; ++w) M = fmaxf(M, S.m[w][w == w0 ? slot0 : 0][rr]);
             const float ref = M == -INFINITY ? 0.0f : M;
             float z = 0.0f;
             float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(wm[w][rr] - ref);
-                const float4 x = *reinterpret_cast<const float4 *>(merge + (w * kRows + rr) * kPD + 4 * lane);
-                z = fmaf(f, wz[w][rr], z);
-                o.x = fmaf(f, x.x, o.x);
-                o.y = fmaf(f, x.y, o.y);
-                o.z = fmaf(f, x.z, o.z);
-                o.w = fmaf(f, x.w, o.w);
+            for (int w = w0; w <= w1; ++w) {
+                const int slot = w == w0 ? slot0 : 0;
+                const float *src = slot == 0 ? S.first[w]
+                                             : reinterpret_cast<const float *>(ring + w * kStages * kStageBytes);
+                add_scaled(o, z, ex2(S.m[w][slot][rr] - ref), *reinterpret_cast<const float4 *>(src + rr * kPD + 4 * lane),
+                           S.z[w][slot][rr]);
             }
             if (complete) {
-                const float iz = z > 0.0f ? 1.0f / z : 0.0f;
-                *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(s.start + row / p.GQ) * p.ldo +
-                                            (head * p.GQ + row % p.GQ) * kPD + 4 * lane) =
-                    make_float4(o.x * iz, o.y * iz, o.z * iz, o.w * iz);
+                write_row(p, s.start, pc.head, row, o, z, 4 * lane);
             } else {
+                float *rec = p.part + static_cast<int64_t>(2 * c + slot0) * kRecFloats;
                 *reinterpret_cast<float4 *>(rec + rr * kPD + 4 * lane) = o;
-                if (lane == 0) {
-                    rec[kRows * kPD + 2 * rr] = M;
-                    rec[kRows * kPD + 2 * rr + 1] = z;
-                }
+                if (lane == 0) *reinterpret_cast<float2 *>(rec + kRows * kPD + 2 * rr) = make_float2(M, z);
             }
         }
+    }
 
-        // ---- a cut item: whoever finishes its last part merges all of them
-        if (!complete) {
-            // the ranges that hold its first and its last tile (range c begins at floor(c * total / G))
-            const int c_first = static_cast<int>(((item_u0 + 1) * G + total - 1) / total) - 1;
-            const int c_last = static_cast<int>(((item_u0 + item_units) * G + total - 1) / total) - 1;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int done = atomicAdd(p.counters + c_first, 1);
-                s_last = done == c_last - c_first;
-                if (s_last) p.counters[c_first] = 0;  // zero at rest
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                for (int rr = warp; rr < kRows; rr += kWarps) {
-                    const int row = kRows * rt + rr;
-                    if (row >= s.rows) break;
-                    const int parts = c_last - c_first + 1;
-                    auto record = [&](int i) {
-                        return p.part + static_cast<int64_t>(i == 0 ? 2 * c_first + 1 : 2 * (c_first + i)) * kRecFloats;
-                    };
-                    float M = -INFINITY;
-                    for (int i = lane; i < parts; i += 32)
-                        M = fmaxf(M, __ldcg(record(i) + kRows * kPD + 2 * rr));
-                    M = warp_max(M);
-                    const float ref = M == -INFINITY ? 0.0f : M;
-                    float z = 0.0f;
-                    float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-                    for (int i = 0; i < parts; ++i) {
-                        const float *rc = record(i);
-                        const float2 mz = __ldcg(reinterpret_cast<const float2 *>(rc + kRows * kPD + 2 * rr));
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(rc + rr * kPD + 4 * lane));
-                        const float f = ex2(mz.x - ref);
-                        z = fmaf(f, mz.y, z);
-                        o.x = fmaf(f, x.x, o.x);
-                        o.y = fmaf(f, x.y, o.y);
-                        o.z = fmaf(f, x.z, o.z);
-                        o.w = fmaf(f, x.w, o.w);
-                    }
-                    const float iz = z > 0.0f ? 1.0f / z : 0.0f;
-                    *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(s.start + row / p.GQ) * p.ldo +
-                                                (head * p.GQ + row % p.GQ) * kPD + 4 * lane) =
-                        make_float4(o.x * iz, o.y * iz, o.z * iz, o.w * iz);
-                }
+    // ---- an item cut between CTAs: whoever finishes its last part merges all
+    if (cut[0] || cut[1]) {
+        __threadfence();
+        __syncthreads();
+        int first[2], parts[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            first[a] = parts[a] = 0;
+            if (!cut[a]) continue;
+            first[a] = R.owner(shared_piece[a].u0) / kWarps;
+            parts[a] = R.owner(shared_piece[a].u0 + shared_piece[a].units - 1) / kWarps - first[a] + 1;
+            if (tid == 32 * a) {
+                const int done = atomicAdd(p.counters + first[a], 1);
+                S.last[a] = done + 1 == parts[a];
+                if (done + 1 == parts[a]) p.counters[first[a]] = 0;  // zero at rest
             }
         }
-        u += k1 - k0;
-        off += k1 - k0;
-        __syncthreads();  // the merge buffer and the shared words are free
+        __syncthreads();
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            if (!cut[a] || !S.last[a]) continue;
+            __threadfence();
+            const Piece &pc = shared_piece[a];
+            const Seq s = sequence(p, pc.b);
+            for (int rr = warp; rr < kRows; rr += kWarps) {
+                const int row = kRows * pc.rt + rr;
+                if (row >= s.rows) break;
+                auto record = [&](int i) {
+                    return p.part + static_cast<int64_t>(2 * (first[a] + i) + (i == 0 ? 1 : 0)) * kRecFloats;
+                };
+                float z = 0.0f, M = -INFINITY;
+                float4 o = make_float4(0, 0, 0, 0);
+                for (int i0 = 0; i0 < parts[a]; i0 += 32) {  // 32 parts at a time: one (m, z) a lane
+                    const int n = min(32, parts[a] - i0);
+                    float2 mz = make_float2(-INFINITY, 0.0f);
+                    if (lane < n) mz = __ldcg(reinterpret_cast<const float2 *>(record(i0 + lane) + kRows * kPD + 2 * rr));
+                    const float Mn = fmaxf(M, warp_max(mz.x));
+                    const float ref = Mn == -INFINITY ? 0.0f : Mn;
+                    const float back = ex2(M - ref);
+                    z *= back;
+                    o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
+                    M = Mn;
+                    const float f = ex2(mz.x - ref);
+#pragma unroll 8
+                    for (int i = 0; i < n; ++i) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(record(i0 + i) + rr * kPD + 4 * lane));
+                        add_scaled(o, z, __shfl_sync(0xffffffffu, f, i), x, __shfl_sync(0xffffffffu, mz.y, i));
+                    }
+                }
+                write_row(p, s.start, pc.head, row, o, z, 4 * lane);
+            }
+        }
     }
     pdl_launch_dependents();
 }
-
-constexpr size_t kSplitSmem = kWarps * kStages * kStageBytes + 1024;
 
 template <int KIND>
 cudaError_t launch_split(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int ctas, cudaStream_t s) {
@@ -597,12 +713,12 @@ cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s
         *why = "cuTensorMapEncodeTiled failed or is unavailable";
         return cudaErrorInvalidValue;
     }
-    // one CTA per resident slot, fewer when the tiles are few
+    // one CTA per SM, fewer when the tiles are few
     const int64_t rowtiles = ceil_div(static_cast<int64_t>(std::min(A.batch.max_rows, A.batch.T)) * p.GQ, kRows);
     const int64_t span = A.window > 0 ? std::min<int64_t>(A.batch.max_ctx, static_cast<int64_t>(A.window) + A.sinks + 32)
                                       : A.batch.max_ctx;
     const int64_t units = std::min<int64_t>(A.batch.B, A.batch.T) * A.cache.Hkv * rowtiles * ceil_div(span, kPB);
-    int64_t ctas = std::min<int64_t>(kCtasPerSm * A.num_sms, ceil_div(units, kWarps));
+    int64_t ctas = std::min<int64_t>(A.num_sms, ceil_div(units, kWarps));
     ctas = std::max<int64_t>(1, std::min<int64_t>(ctas, kMaxCtas));
     if (A.cache.kind == TERN_KV_INT8) return launch_split<TERN_KV_INT8>(p, km, vm, static_cast<int>(ctas), s);
     return launch_split<TERN_KV_E4M3>(p, km, vm, static_cast<int>(ctas), s);
