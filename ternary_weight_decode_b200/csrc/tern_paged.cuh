@@ -15,8 +15,26 @@ constexpr int kPD = 128;                 // head dimension
 constexpr int kPB = TERN_KV_BLOCK;       // tokens that share a scale
 constexpr int kMaxBatch = 4096;          // sequences of a batch
 
+// Division of 0 <= n < 2^31 by a number fixed at the launch: multiply, add,
+// shift (with l = ceil(log2 d): mul = floor(2^32 (2^l - d) / d) + 1).
+struct FastDiv {
+    uint32_t d, mul, shift;
+    __device__ __forceinline__ int quot(int n) const {
+        return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+    }
+};
+inline FastDiv fast_div(int d) {
+    FastDiv f;
+    f.d = static_cast<uint32_t>(d);
+    f.shift = 0;
+    while ((1ull << f.shift) < f.d) ++f.shift;
+    f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.shift) - f.d)) / f.d + 1);
+    return f;
+}
+
 struct PagedView {
     int kind, Hkv, page_size, bpp, n_pages;  // bpp: blocks of 16 tokens per page
+    FastDiv by_bpp;
     uint8_t *kc, *vc;
     float *ks, *vs;
     int B, T, pages_ld;
@@ -29,6 +47,7 @@ inline PagedView paged_view(const tern_paged_batch &B, const tern_paged_cache &C
     v.Hkv = C.Hkv;
     v.page_size = C.page_size;
     v.bpp = C.page_size / kPB;
+    v.by_bpp = fast_div(v.bpp);
     v.n_pages = C.n_pages;
     v.kc = C.k_codes;
     v.vc = C.v_codes;
@@ -48,8 +67,9 @@ inline PagedView paged_view(const tern_paged_batch &B, const tern_paged_cache &C
 // the page table has no valid page there.  Head g lies g * bpp further on, and
 // the codes of the block start at 2048 times its index.
 __device__ __forceinline__ int64_t block_index(const PagedView &v, int b, int blk) {
-    const int e = blk / v.bpp;
-    if (blk < 0 || e >= v.pages_ld) return -1;
+    if (blk < 0) return -1;
+    const int e = v.by_bpp.quot(blk);
+    if (e >= v.pages_ld) return -1;
     const int page = v.pages[static_cast<int64_t>(b) * v.pages_ld + e];
     if (page < 0 || page >= v.n_pages) return -1;
     return static_cast<int64_t>(page) * v.Hkv * v.bpp + (blk - e * v.bpp);

@@ -46,6 +46,7 @@ constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 8;         // rows of an item
 constexpr int kStages = 3;       // tiles in flight per warp
+constexpr int kBatch = 16;       // tiles whose places are looked up at a time, one a lane
 constexpr int kTileBytes = kPB * kPD;       // 2048: one block's codes of K or of V
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kMaxCtas = 1024;   // CTAs of a launch (counters of the workspace)
@@ -58,6 +59,7 @@ struct AttnParams {
     PagedView v;
     const float *q;
     int ldq, Hq, GQ;
+    FastDiv by_gq;
     int window, sinks;
     float scale_log2;
     float *out;
@@ -92,7 +94,7 @@ struct Tiles {
 
 __device__ __forceinline__ Tiles tiles_of(const AttnParams &p, const Seq &s, int rt) {
     const int r1 = min(kRows * rt + kRows, s.rows) - 1;
-    const int p0 = s.first + kRows * rt / p.GQ, p1 = s.first + r1 / p.GQ;
+    const int p0 = s.first + p.by_gq.quot(kRows * rt), p1 = s.first + p.by_gq.quot(r1);
     const int hi = max(0, min(p1 + 1, s.end));
     const int hit = (hi + kPB - 1) / kPB;
     Tiles t;
@@ -125,6 +127,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
@@ -162,7 +173,7 @@ __device__ __forceinline__ uint32_t flip(uint32_t w) {
 // lane's output columns (dimensions 32 t + i and 32 t + 16 + i).
 struct State {
     float m, z;
-    float o[16][2];
+    float2 o[16];
 };
 
 // Quotient of nonnegative numbers; 64-bit division is a long routine that
@@ -192,7 +203,8 @@ struct Cursor {
     __device__ __forceinline__ int tile() const { return k < tl.sink ? k : tl.lo + k - tl.sink; }
 };
 
-__device__ __forceinline__ void advance(const AttnParams &p, Cursor &x, int n) {
+template <typename SeqOf>
+__device__ __forceinline__ void advance(const AttnParams &p, Cursor &x, int n, SeqOf seq_of) {
     x.k += n;
     while (x.k >= x.units()) {
         x.k -= x.units();
@@ -204,7 +216,7 @@ __device__ __forceinline__ void advance(const AttnParams &p, Cursor &x, int n) {
                 x.head = 0;
                 do {
                     if (++x.b >= p.v.B) return;  // past the line: the caller counts its tiles
-                    x.s = sequence(p, x.b);
+                    x.s = seq_of(x.b);
                 } while (x.s.rows == 0);
             }
         }
@@ -232,11 +244,12 @@ constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kPieceFloats = kRows * kPD;
 struct SplitShared {
     float first[kWarps][kPieceFloats];  // the piece a warp's range begins with (its last piece lies in its ring)
-    TileInfo info[kWarps][2][32];
+    TileInfo info[kWarps][2][kBatch];
     float m[kWarps][2][kRows], z[kWarps][2][kRows];
     Piece piece[kWarps][2];
     uint64_t bars[kWarps][kStages];
     long long chunk[kThreads];          // line index where each thread's sequences begin
+    Seq seq[kThreads];                  // the sequences, when each thread has one at most
     long long scan[kWarps];
     int last[2];
 };
@@ -246,8 +259,9 @@ static_assert(kSplitSmem <= 227 * 1024, "shared memory of one CTA");
 // Row rr of an item to its place in out: four dimensions a lane.
 __device__ __forceinline__ void write_row(const AttnParams &p, int start, int head, int row, float4 o, float z, int d) {
     const float iz = z > 0.0f ? 1.0f / z : 0.0f;
-    *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(start + row / p.GQ) * p.ldo +
-                                (head * p.GQ + row % p.GQ) * kPD + d) =
+    const int i = p.by_gq.quot(row);
+    *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(start + i) * p.ldo +
+                                (head * p.GQ + row - i * p.GQ) * kPD + d) =
         make_float4(o.x * iz, o.y * iz, o.z * iz, o.w * iz);
 }
 
@@ -280,13 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kStages; ++s) mbar_init(&S.bars[warp][s], 1);
         fence_mbar_init();
         S.piece[warp][0].valid = S.piece[warp][1].valid = 0;
+        S.piece[warp][0].ends = 0;
     }
     pdl_wait();
 
     // ---- the line's length, and where each thread's sequences begin on it
     const int per = (v.B + kThreads - 1) / kThreads;
     long long mine = 0;
-    for (int b = tid * per; b < min(v.B, tid * per + per); ++b) mine += v.Hkv * head_units(p, sequence(p, b));
+    for (int b = tid * per; b < min(v.B, tid * per + per); ++b) {
+        const Seq s = sequence(p, b);
+        mine += v.Hkv * head_units(p, s);
+        S.seq[tid] = s;
+    }
+    auto seq_of = [&](int b) { return per == 1 ? S.seq[b] : sequence(p, b); };
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -327,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int b = lo * per;
             long long ph;
             for (;; ++b) {
-                cur.s = sequence(p, b);
+                cur.s = seq_of(b);
                 ph = head_units(p, cur.s);
                 if (off < ph * v.Hkv) break;
                 off -= ph * v.Hkv;
@@ -343,10 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             cur.k = static_cast<int>(off);
         }
-        // each lane keeps its own cursor, 32 tiles apart from its last: tile i of the range is in info[i / 32 % 2][i % 32]
-        if (lane < count) advance(p, cur, lane);
+        // lane l < kBatch keeps the cursor of tiles l, l + kBatch, ...: tile i of the range is in
+        // info[i / kBatch % 2][i % kBatch]
+        auto info = [&](int i) -> TileInfo & { return S.info[warp][(i / kBatch) & 1][i % kBatch]; };
+        if (lane < kBatch && lane < count) advance(p, cur, lane, seq_of);
         auto fill = [&](int i0) {
-            if (i0 + lane < count) {
+            if (lane < kBatch && i0 + lane < count) {
                 TileInfo x;
                 x.j0 = cur.tile() * kPB;
                 x.b = cur.b;
@@ -363,14 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x.vs = v.vs[x.bi];
                     }
                 }
-                S.info[warp][(i0 >> 5) & 1][lane] = x;
-                if (i0 + 32 + lane < count) advance(p, cur, 32);
+                info(i0 + lane) = x;
+                if (i0 + kBatch + lane < count) advance(p, cur, kBatch, seq_of);
             }
             __syncwarp();
         };
         auto start = [&](int i) {  // tile i's copies into its stage
             if (lane == 0 && i < count) {
-                const int bi = S.info[warp][(i >> 5) & 1][i & 31].bi;
+                const int bi = info(i).bi;
                 if (bi >= 0) {
                     uint8_t *dst = my_ring + (i % kStages) * kStageBytes;
                     uint64_t *bar = &S.bars[warp][i % kStages];
@@ -383,7 +405,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fill(0);
 #pragma unroll
         for (int i = 0; i < kStages; ++i) start(i);
-        fill(32);
 
         State st;
         uint32_t qhi[8][2], qlo[8][2];
@@ -393,19 +414,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phases = 0;  // parity of each stage
         int stage = 0;
         for (int i = 0; i < count; ++i) {
-            if ((i & 31) == 0 && i > 0) fill(i + 32);
-            const TileInfo x = S.info[warp][(i >> 5) & 1][i & 31];
+            const TileInfo x = info(i);
             if (i == 0 || (x.k >> 1) == 0) {
                 // ---- a new item: row g's query, dimensions 32 t .. 32 t + 31, as hi + lo operands
-                s = sequence(p, x.b);
+                s = seq_of(x.b);
                 k_first = x.k >> 1;
                 const int r = kRows * x.rt + g;
                 const bool row_ok = r < s.rows;
-                pos = s.first + (row_ok ? r / p.GQ : 0);
-                p_min = s.first + kRows * x.rt / p.GQ;
-                p_max = s.first + (min(kRows * x.rt + kRows, s.rows) - 1) / p.GQ;
-                const float *qp = p.q + static_cast<int64_t>(s.start + r / p.GQ) * p.ldq +
-                                  (x.head * p.GQ + r % p.GQ) * kPD + 32 * t;
+                const int ri = row_ok ? p.by_gq.quot(r) : 0;
+                pos = s.first + ri;
+                p_min = s.first + p.by_gq.quot(kRows * x.rt);
+                p_max = s.first + p.by_gq.quot(min(kRows * x.rt + kRows, s.rows) - 1);
+                const float *qp = p.q + static_cast<int64_t>(s.start + ri) * p.ldq +
+                                  (x.head * p.GQ + (row_ok ? r : 0) - ri * p.GQ) * kPD + 32 * t;
                 float4 q4[8];
                 float amax = 0.0f;
 #pragma unroll
@@ -427,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st.m = -INFINITY;
                 st.z = 0.0f;
 #pragma unroll
-                for (int n = 0; n < 16; ++n) st.o[n][0] = st.o[n][1] = 0.0f;
+                for (int n = 0; n < 16; ++n) st.o[n] = make_float2(0.0f, 0.0f);
             }
             if (x.bi >= 0) {
                 mbar_wait_bounded(&S.bars[warp][stage], (phases >> stage) & 1u);
@@ -474,10 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float corr = ex2(st.m - ref);  // 0 when nothing was seen before
                     st.z *= corr;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        st.o[k][0] *= corr;
-                        st.o[k][1] *= corr;
-                    }
+                    for (int k = 0; k < 16; ++k) st.o[k] = __fmul2_rn(st.o[k], make_float2(corr, corr));
                     st.m = mn;
                 }
                 float w[4];
@@ -508,19 +526,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t yl = __byte_perm(y0, y1, 0x5140), yh = __byte_perm(y0, y1, 0x7362);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        if (e == 0) mma_f16(d, a, code_pair<KIND, 0>(xl), code_pair<KIND, 0>(yl));
-                        if (e == 1) mma_f16(d, a, code_pair<KIND, 1>(xl), code_pair<KIND, 1>(yl));
-                        if (e == 2) mma_f16(d, a, code_pair<KIND, 0>(xh), code_pair<KIND, 0>(yh));
-                        if (e == 3) mma_f16(d, a, code_pair<KIND, 1>(xh), code_pair<KIND, 1>(yh));
-                        float(&o)[2] = st.o[4 * q4 + e];
-                        o[0] = fmaf(x.vs, d[0] + d[2], o[0]);
-                        o[1] = fmaf(x.vs, d[1] + d[3], o[1]);
+                        float d[4];
+                        if (e == 0) mma_f16_zero(d, a, code_pair<KIND, 0>(xl), code_pair<KIND, 0>(yl));
+                        if (e == 1) mma_f16_zero(d, a, code_pair<KIND, 1>(xl), code_pair<KIND, 1>(yl));
+                        if (e == 2) mma_f16_zero(d, a, code_pair<KIND, 0>(xh), code_pair<KIND, 0>(yh));
+                        if (e == 3) mma_f16_zero(d, a, code_pair<KIND, 1>(xh), code_pair<KIND, 1>(yh));
+                        const float2 sum = __fadd2_rn(make_float2(d[0], d[1]), make_float2(d[2], d[3]));
+                        st.o[4 * q4 + e] = __ffma2_rn(make_float2(x.vs, x.vs), sum, st.o[4 * q4 + e]);
                     }
                 }
                 fence_proxy_async_smem();  // these reads before the refill of the stage
                 __syncwarp();
             }
+            // the tiles behind the next batch's, while this one's are worked off (at tile 0 behind its queries)
+            if (i % kBatch == 0 && i + kBatch < count) fill(i + kBatch);
             start(i + kStages);
             stage = stage + 1 == kStages ? 0 : stage + 1;
 
@@ -533,22 +552,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (k_first == 0 && ends) {
                     if (r < s.rows) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int n = 0; n < 16; n += 4)
-                                write_row(p, s.start, x.head, r,
-                                          make_float4(st.o[n][e], st.o[n + 1][e], st.o[n + 2][e], st.o[n + 3][e]), st.z,
-                                          32 * t + 16 * e + n);
+                        for (int n = 0; n < 16; n += 4) {
+                            write_row(p, s.start, x.head, r,
+                                      make_float4(st.o[n].x, st.o[n + 1].x, st.o[n + 2].x, st.o[n + 3].x), st.z, 32 * t + n);
+                            write_row(p, s.start, x.head, r,
+                                      make_float4(st.o[n].y, st.o[n + 1].y, st.o[n + 2].y, st.o[n + 3].y), st.z,
+                                      32 * t + 16 + n);
+                        }
                     }
                 } else {
                     const int slot = k_first > 0 ? 0 : 1;  // a range's first piece, or its last
                     float *dst = (slot == 0 ? S.first[warp] : reinterpret_cast<float *>(my_ring)) + g * kPD + 32 * t;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int n = 0; n < 16; n += 4)
-                            *reinterpret_cast<float4 *>(dst + 16 * e + n) =
-                                make_float4(st.o[n][e], st.o[n + 1][e], st.o[n + 2][e], st.o[n + 3][e]);
+                    for (int n = 0; n < 16; n += 4) {
+                        *reinterpret_cast<float4 *>(dst + n) =
+                            make_float4(st.o[n].x, st.o[n + 1].x, st.o[n + 2].x, st.o[n + 3].x);
+                        *reinterpret_cast<float4 *>(dst + 16 + n) =
+                            make_float4(st.o[n].y, st.o[n + 1].y, st.o[n + 2].y, st.o[n + 3].y);
+                    }
                     if (t == 0) {
                         S.m[warp][slot][g] = st.m;
                         S.z[warp][slot][g] = st.z;
@@ -575,33 +596,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the first pieces of the warps behind it until the item ends
     bool cut[2] = {false, false};  // groups that other CTAs share: begun before this CTA, going on behind it
     Piece shared_piece[2];
-    for (int a = -1; a < kWarps; ++a) {
-        const int w0 = max(a, 0), slot0 = a < 0 ? 0 : 1;
-        const Piece &pc = S.piece[w0][slot0];
-        if (!pc.valid) continue;
-        int w1 = w0;  // last warp of the group
+    const bool is_warp = lane < kWarps;
+    const unsigned first_ok = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].valid);
+    const unsigned first_ends = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].ends);
+    const unsigned last_ok = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][1].valid);
+    // bit 0: the first piece of warp 0, bit a + 1: the last piece of warp a
+    for (unsigned groups = (first_ok & 1u) | last_ok << 1; groups != 0; groups &= groups - 1) {
+        const int a = __ffs(groups) - 2, w0 = max(a, 0), slot0 = a < 0 ? 0 : 1;
+        const Piece pc = S.piece[w0][slot0];
+        // last warp of the group: the first behind w0 whose first piece ends the item, or whose neighbour has none
         bool ends = pc.ends;
-        while (!ends && w1 + 1 < kWarps && S.piece[w1 + 1][0].valid) ends = S.piece[++w1][0].ends;
+        int w1 = w0;
+        while (!ends && w1 + 1 < kWarps && (first_ok >> (w1 + 1) & 1u)) ends = first_ends >> ++w1 & 1u;
         const bool complete = a >= 0 && ends;
         if (!complete) {
             cut[slot0] = true;
             shared_piece[slot0] = pc;
         }
-        const Seq s = sequence(p, pc.b);
+        const Seq s = seq_of(pc.b);
         for (int rr = warp; rr < kRows; rr += kWarps) {
             const int row = kRows * pc.rt + rr;
             if (row >= s.rows) break;
-            float M = -INFINITY;
-            for (int w = w0; w <= w1; ++w) M = fmaxf(M, S.m[w][w == w0 ? slot0 : 0][rr]);
-            const float ref = M == -INFINITY ? 0.0f : M;
-            float z = 0.0f;
+            const bool mine = lane >= w0 && lane <= w1;
+            const int slot = lane == w0 ? slot0 : 0;
+            const float m = mine ? S.m[lane][slot][rr] : -INFINITY;
+            const float M = warp_max(m);
+            const float f = ex2(m - (M == -INFINITY ? 0.0f : M));
+            const float z = warp_sum(mine ? f * S.z[lane][slot][rr] : 0.0f);
             float4 o = make_float4(0, 0, 0, 0);
+            float unused = 0.0f;
+#pragma unroll 4
             for (int w = w0; w <= w1; ++w) {
-                const int slot = w == w0 ? slot0 : 0;
-                const float *src = slot == 0 ? S.first[w]
-                                             : reinterpret_cast<const float *>(ring + w * kStages * kStageBytes);
-                add_scaled(o, z, ex2(S.m[w][slot][rr] - ref), *reinterpret_cast<const float4 *>(src + rr * kPD + 4 * lane),
-                           S.z[w][slot][rr]);
+                const float *src = w == w0 && slot0 == 1 ? reinterpret_cast<const float *>(ring + w * kStages * kStageBytes)
+                                                         : S.first[w];
+                add_scaled(o, unused, __shfl_sync(0xffffffffu, f, w),
+                           *reinterpret_cast<const float4 *>(src + rr * kPD + 4 * lane), 0.0f);
             }
             if (complete) {
                 write_row(p, s.start, pc.head, row, o, z, 4 * lane);
@@ -636,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!cut[a] || !S.last[a]) continue;
             __threadfence();
             const Piece &pc = shared_piece[a];
-            const Seq s = sequence(p, pc.b);
+            const Seq s = seq_of(pc.b);
             for (int rr = warp; rr < kRows; rr += kWarps) {
                 const int row = kRows * pc.rt + rr;
                 if (row >= s.rows) break;
@@ -699,6 +728,7 @@ cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s
     p.ldq = A.ldq;
     p.Hq = A.Hq;
     p.GQ = A.Hq / A.cache.Hkv;
+    p.by_gq = fast_div(p.GQ);
     p.window = std::min(A.window, 1 << 30);  // positions minus a window stay in 32 bits
     p.sinks = std::min(A.sinks, 1 << 30);
     p.scale_log2 = A.scale * 1.4426950408889634f;
