@@ -27,7 +27,8 @@ LIBS = {
     "libtern_synth.so": ["synth_csrc/tern_synth.cu"],
 }
 HEADERS = ["csrc/tern_common.cuh", "csrc/tern_internal.h", "csrc/tern_tc.cuh",
-           "csrc/tern_gemv_common.cuh", "csrc/tern_gemv_stream.cuh", "csrc/tern_paged.cuh"]
+           "csrc/tern_gemv_common.cuh", "csrc/tern_gemv_stream.cuh", "csrc/tern_paged.cuh",
+           "csrc/tern_paged_attention.cuh"]
 
 
 def _newest(paths):

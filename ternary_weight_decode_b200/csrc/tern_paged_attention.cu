@@ -36,7 +36,7 @@
 
 #include <algorithm>
 
-#include "tern_paged.cuh"
+#include "tern_paged_attention.cuh"
 
 namespace tern {
 
@@ -49,77 +49,7 @@ constexpr int kStages = 3;       // tiles in flight per warp
 constexpr int kBatch = 16;       // tiles whose places are looked up at a time, one a lane
 constexpr int kTileBytes = kPB * kPD;       // 2048: one block's codes of K or of V
 constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kMaxCtas = 1024;   // CTAs of a launch (counters of the workspace)
 constexpr float kPScale = 8.0f;  // softmax weights are held times 2^8: their lo parts stay normal in fp16
-
-// Workspace: kMaxCtas counters (zero at rest), then per CTA two partial records.
-constexpr int kRecFloats = kRows * (kPD + 2);
-
-struct AttnParams {
-    PagedView v;
-    const float *q;
-    int ldq, Hq, GQ;
-    FastDiv by_gq;
-    int window, sinks;
-    float scale_log2;
-    float *out;
-    int ldo;
-    int *counters;
-    float *part;
-};
-
-// One sequence as this call sees it.
-struct Seq {
-    int start, rows;  // first row, rows x query heads of a group
-    int first;        // token of the first row
-    int end;          // tokens that may be read: min(ctx, page table)
-};
-
-__device__ __forceinline__ Seq sequence(const AttnParams &p, int b) {
-    const PagedView &v = p.v;
-    const int s0 = v.row_start[b], s1 = v.row_start[b + 1], ctx = v.ctx[b];
-    Seq s;
-    s.start = s0;
-    s.rows = s0 < 0 || s0 > v.T || s1 <= s0 ? 0 : (min(s1, v.T) - s0) * p.GQ;
-    s.first = ctx - (s1 - s0);
-    const long long cap = static_cast<long long>(v.pages_ld) * v.page_size;
-    s.end = static_cast<int>(min(static_cast<long long>(min(ctx, 0x7FFFFF00)), cap));
-    return s;
-}
-
-// Visible tiles of row tile rt: tile k is k below `sink`, else lo + k - sink.
-struct Tiles {
-    int n, sink, lo;
-};
-
-__device__ __forceinline__ Tiles tiles_of(const AttnParams &p, const Seq &s, int rt) {
-    const int r1 = min(kRows * rt + kRows, s.rows) - 1;
-    const int p0 = s.first + p.by_gq.quot(kRows * rt), p1 = s.first + p.by_gq.quot(r1);
-    const int hi = max(0, min(p1 + 1, s.end));
-    const int hit = (hi + kPB - 1) / kPB;
-    Tiles t;
-    t.lo = t.sink = 0;
-    if (p.window > 0) {
-        t.lo = min(max(0, p0 - p.window + 1) / kPB, hit);
-        t.sink = min((min(p.sinks, hi) + kPB - 1) / kPB, t.lo);
-    }
-    t.n = t.sink + hit - t.lo;
-    return t;
-}
-
-// Tiles of one KV head of a sequence (an item that sees nothing still counts
-// one: its rows are written as 0).
-__device__ __forceinline__ long long head_units(const AttnParams &p, const Seq &s) {
-    long long u = 0;
-    for (int rt = 0; rt * kRows < s.rows; ++rt) u += max(1, tiles_of(p, s, rt).n);
-    return u;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -176,54 +106,6 @@ struct State {
     float2 o[16];
 };
 
-// Quotient of nonnegative numbers; 64-bit division is a long routine that
-// nearly every call can do without.
-__device__ __forceinline__ long long quot(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-// The line of `total` tiles in n ranges: the first `more` hold base + 1 tiles,
-// the others base (n <= total, so none is empty).
-struct Ranges {
-    long long base, more;
-    __device__ __forceinline__ long long begin(int i) const { return base * i + min(static_cast<long long>(i), more); }
-    __device__ __forceinline__ int owner(long long u) const {
-        const long long big = more * (base + 1);
-        return static_cast<int>(u < big ? quot(u, base + 1) : more + quot(u - big, base));
-    }
-};
-
-// A place on the line: tile k of an item.
-struct Cursor {
-    int b, head, rt, k;
-    Seq s;
-    Tiles tl;
-    __device__ __forceinline__ int units() const { return max(1, tl.n); }
-    __device__ __forceinline__ int tile() const { return k < tl.sink ? k : tl.lo + k - tl.sink; }
-};
-
-template <typename SeqOf>
-__device__ __forceinline__ void advance(const AttnParams &p, Cursor &x, int n, SeqOf seq_of) {
-    x.k += n;
-    while (x.k >= x.units()) {
-        x.k -= x.units();
-        if ((x.rt + 1) * kRows < x.s.rows) {
-            ++x.rt;
-        } else {
-            x.rt = 0;
-            if (++x.head == p.v.Hkv) {
-                x.head = 0;
-                do {
-                    if (++x.b >= p.v.B) return;  // past the line: the caller counts its tiles
-                    x.s = seq_of(x.b);
-                } while (x.s.rows == 0);
-            }
-        }
-        x.tl = tiles_of(p, x.s, x.rt);
-    }
-}
-
 // What a warp's walk needs of one tile.
 struct __align__(16) TileInfo {
     int bi;          // scale block of K and V (its 16 rows begin at 16 bi), -1: none
@@ -231,13 +113,6 @@ struct __align__(16) TileInfo {
     int j0;          // first token
     int b, head, rt; // item
     int k;           // tile of the item, times 2, + 1 for the item's last tile
-};
-
-// A piece of a cut item.
-struct Piece {
-    int valid, ends;   // ends: holds the item's last tile
-    int b, head, rt, units;
-    long long u0;      // line index of the item's first tile
 };
 
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
@@ -248,30 +123,11 @@ struct SplitShared {
     float m[kWarps][2][kRows], z[kWarps][2][kRows];
     Piece piece[kWarps][2];
     uint64_t bars[kWarps][kStages];
-    long long chunk[kThreads];          // line index where each thread's sequences begin
-    Seq seq[kThreads];                  // the sequences, when each thread has one at most
-    long long scan[kWarps];
+    LineShared<kThreads> line;
     int last[2];
 };
 constexpr size_t kSplitSmem = kRingBytes + sizeof(SplitShared) + 1024;
 static_assert(kSplitSmem <= 227 * 1024, "shared memory of one CTA");
-
-// Row rr of an item to its place in out: four dimensions a lane.
-__device__ __forceinline__ void write_row(const AttnParams &p, int start, int head, int row, float4 o, float z, int d) {
-    const float iz = z > 0.0f ? 1.0f / z : 0.0f;
-    const int i = p.by_gq.quot(row);
-    *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(start + i) * p.ldo +
-                                (head * p.GQ + row - i * p.GQ) * kPD + d) =
-        make_float4(o.x * iz, o.y * iz, o.z * iz, o.w * iz);
-}
-
-__device__ __forceinline__ void add_scaled(float4 &o, float &z, float f, float4 x, float xz) {
-    z = fmaf(f, xz, z);
-    o.x = fmaf(f, x.x, o.x);
-    o.y = fmaf(f, x.y, o.y);
-    o.z = fmaf(f, x.z, o.z);
-    o.w = fmaf(f, x.w, o.w);
-}
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -298,31 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
 
-    // ---- the line's length, and where each thread's sequences begin on it
-    const int per = (v.B + kThreads - 1) / kThreads;
-    long long mine = 0;
-    for (int b = tid * per; b < min(v.B, tid * per + per); ++b) {
-        const Seq s = sequence(p, b);
-        mine += v.Hkv * head_units(p, s);
-        S.seq[tid] = s;
-    }
-    auto seq_of = [&](int b) { return per == 1 ? S.seq[b] : sequence(p, b); };
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-    }
-    if (lane == 31) S.scan[warp] = incl;
-    __syncthreads();
-    long long total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += S.scan[w];
-        total += S.scan[w];
-    }
-    S.chunk[tid] = before + incl - mine;
-    __syncthreads();
+    // ---- the line of tiles, and this warp's range of it
+    const Line L = make_line<kRows, 1>(p, S.line);
+    const long long total = L.total;
+    auto seq_of = [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); };
     const int nw = static_cast<int>(min(static_cast<long long>(gridDim.x) * kWarps, total));
     Ranges R = {0, 0};
     if (total > 0) {
@@ -334,43 +169,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int count = wi < nw ? static_cast<int>(R.begin(wi + 1) - u0) : 0;
 
     if (count > 0) {
-        // ---- the range's first tile
-        Cursor cur;
-        {
-            int lo = 0;  // the last thread whose sequences begin at or before u0: 12 probes a lane, one ballot each
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const unsigned le = __ballot_sync(0xffffffffu, S.chunk[32 * i + lane] <= u0);
-                if (le) lo = 32 * i + 31 - __clz(le);
-            }
-            long long off = u0 - S.chunk[lo];
-            int b = lo * per;
-            long long ph;
-            for (;; ++b) {
-                cur.s = seq_of(b);
-                ph = head_units(p, cur.s);
-                if (off < ph * v.Hkv) break;
-                off -= ph * v.Hkv;
-            }
-            cur.b = b;
-            cur.head = static_cast<int>(quot(off, ph));
-            off -= cur.head * ph;
-            cur.rt = 0;
-            cur.tl = tiles_of(p, cur.s, 0);
-            while (off >= cur.units()) {
-                off -= cur.units();
-                cur.tl = tiles_of(p, cur.s, ++cur.rt);
-            }
-            cur.k = static_cast<int>(off);
-        }
+        Cursor<1> cur = find_place<kRows, 1>(p, S.line, L, u0, seq_of);
         // lane l < kBatch keeps the cursor of tiles l, l + kBatch, ...: tile i of the range is in
         // info[i / kBatch % 2][i % kBatch]
         auto info = [&](int i) -> TileInfo & { return S.info[warp][(i / kBatch) & 1][i % kBatch]; };
-        if (lane < kBatch && lane < count) advance(p, cur, lane, seq_of);
+        if (lane < kBatch && lane < count) advance<kRows>(p, cur, lane, seq_of);
         auto fill = [&](int i0) {
             if (lane < kBatch && i0 + lane < count) {
                 TileInfo x;
-                x.j0 = cur.tile() * kPB;
+                x.j0 = cur.tl.block(cur.k) * kPB;
                 x.b = cur.b;
                 x.head = cur.head;
                 x.rt = cur.rt;
@@ -378,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x.bi = -1;
                 x.ks = x.vs = 0.0f;
                 if (cur.tl.n > 0) {
-                    const int64_t bi = block_index(v, cur.b, cur.tile());
+                    const int64_t bi = block_index(v, cur.b, cur.tl.block(cur.k));
                     if (bi >= 0) {
                         x.bi = static_cast<int>(bi) + cur.head * v.bpp;
                         x.ks = v.ks[x.bi];
@@ -386,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 info(i0 + lane) = x;
-                if (i0 + kBatch + lane < count) advance(p, cur, kBatch, seq_of);
+                if (i0 + kBatch + lane < count) advance<kRows>(p, cur, kBatch, seq_of);
             }
             __syncwarp();
         };
@@ -582,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pc.head = x.head;
                         pc.rt = x.rt;
                         pc.u0 = u0 + i - (x.k >> 1);
-                        pc.units = max(1, tiles_of(p, s, x.rt).n);
+                        pc.units = tile_count<1>(tiles_of<kRows>(p, s, x.rt));
                         S.piece[warp][slot] = pc;
                     }
                 }
@@ -595,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (a = warp) or with the first piece of warp 0 (a = -1), and goes on with
     // the first pieces of the warps behind it until the item ends
     bool cut[2] = {false, false};  // groups that other CTAs share: begun before this CTA, going on behind it
-    Piece shared_piece[2];
+    Piece shared_piece[2] = {};
     const bool is_warp = lane < kWarps;
     const unsigned first_ok = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].valid);
     const unsigned first_ends = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].ends);
@@ -604,14 +411,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (unsigned groups = (first_ok & 1u) | last_ok << 1; groups != 0; groups &= groups - 1) {
         const int a = __ffs(groups) - 2, w0 = max(a, 0), slot0 = a < 0 ? 0 : 1;
         const Piece pc = S.piece[w0][slot0];
-        // last warp of the group: the first behind w0 whose first piece ends the item, or whose neighbour has none
+        // last warp of the group: the first behind w0 whose first piece ends the item, else the last of those that have one
         bool ends = pc.ends;
         int w1 = w0;
-        while (!ends && w1 + 1 < kWarps && (first_ok >> (w1 + 1) & 1u)) ends = first_ends >> ++w1 & 1u;
+        if (!ends) {
+            const int run = __ffs(~(first_ok >> (w0 + 1))) - 1, e = __ffs(first_ends >> (w0 + 1));
+            ends = e != 0 && e <= run;
+            w1 += ends ? e : run;
+        }
         const bool complete = a >= 0 && ends;
         if (!complete) {
-            cut[slot0] = true;
-            shared_piece[slot0] = pc;
+            if (slot0 == 0) cut[0] = true; else cut[1] = true;
+            if (slot0 == 0) shared_piece[0] = pc; else shared_piece[1] = pc;
         }
         const Seq s = seq_of(pc.b);
         for (int rr = warp; rr < kRows; rr += kWarps) {
@@ -635,66 +446,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (complete) {
                 write_row(p, s.start, pc.head, row, o, z, 4 * lane);
             } else {
-                float *rec = p.part + static_cast<int64_t>(2 * c + slot0) * kRecFloats;
+                float *rec = p.part + static_cast<int64_t>(2 * c + slot0) * rec_floats(kRows);
                 *reinterpret_cast<float4 *>(rec + rr * kPD + 4 * lane) = o;
                 if (lane == 0) *reinterpret_cast<float2 *>(rec + kRows * kPD + 2 * rr) = make_float2(M, z);
             }
         }
     }
 
-    // ---- an item cut between CTAs: whoever finishes its last part merges all
-    if (cut[0] || cut[1]) {
-        __threadfence();
-        __syncthreads();
-        int first[2], parts[2];
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            first[a] = parts[a] = 0;
-            if (!cut[a]) continue;
-            first[a] = R.owner(shared_piece[a].u0) / kWarps;
-            parts[a] = R.owner(shared_piece[a].u0 + shared_piece[a].units - 1) / kWarps - first[a] + 1;
-            if (tid == 32 * a) {
-                const int done = atomicAdd(p.counters + first[a], 1);
-                S.last[a] = done + 1 == parts[a];
-                if (done + 1 == parts[a]) p.counters[first[a]] = 0;  // zero at rest
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            if (!cut[a] || !S.last[a]) continue;
-            __threadfence();
-            const Piece &pc = shared_piece[a];
-            const Seq s = seq_of(pc.b);
-            for (int rr = warp; rr < kRows; rr += kWarps) {
-                const int row = kRows * pc.rt + rr;
-                if (row >= s.rows) break;
-                auto record = [&](int i) {
-                    return p.part + static_cast<int64_t>(2 * (first[a] + i) + (i == 0 ? 1 : 0)) * kRecFloats;
-                };
-                float z = 0.0f, M = -INFINITY;
-                float4 o = make_float4(0, 0, 0, 0);
-                for (int i0 = 0; i0 < parts[a]; i0 += 32) {  // 32 parts at a time: one (m, z) a lane
-                    const int n = min(32, parts[a] - i0);
-                    float2 mz = make_float2(-INFINITY, 0.0f);
-                    if (lane < n) mz = __ldcg(reinterpret_cast<const float2 *>(record(i0 + lane) + kRows * kPD + 2 * rr));
-                    const float Mn = fmaxf(M, warp_max(mz.x));
-                    const float ref = Mn == -INFINITY ? 0.0f : Mn;
-                    const float back = ex2(M - ref);
-                    z *= back;
-                    o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
-                    M = Mn;
-                    const float f = ex2(mz.x - ref);
-#pragma unroll 8
-                    for (int i = 0; i < n; ++i) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(record(i0 + i) + rr * kPD + 4 * lane));
-                        add_scaled(o, z, __shfl_sync(0xffffffffu, f, i), x, __shfl_sync(0xffffffffu, mz.y, i));
-                    }
-                }
-                write_row(p, s.start, pc.head, row, o, z, 4 * lane);
-            }
-        }
-    }
+    merge_cut_items<kRows, kThreads>(p, cut, shared_piece, R, kWarps, S.last, seq_of);
     pdl_launch_dependents();
 }
 
@@ -717,8 +476,8 @@ cudaError_t launch_split(const AttnParams &p, const CUtensorMap &km, const CUten
 size_t attention_paged_workspace_bytes(int Hq, int Hkv, int num_sms) {
     (void)Hq;
     (void)Hkv;
-    (void)num_sms;
-    return kMaxCtas * sizeof(int) + static_cast<size_t>(2) * kMaxCtas * kRecFloats * sizeof(float);
+    // the counters, and two partial records a CTA (one CTA per SM)
+    return kMaxCtas * sizeof(int) + static_cast<size_t>(2) * std::min(num_sms, kMaxCtas) * rec_floats(kMaxRows) * sizeof(float);
 }
 
 cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s, const char **why) {

@@ -1,0 +1,308 @@
+// tern_paged_attention.cuh -- what the two kernels of the paged attention
+// share: the items of a batch, their visible blocks of 16 tokens, and the line
+// of all their tiles that the grid divides evenly.
+//
+// The rows of one sequence that share a KV head (its tokens times the query
+// heads of the group) are taken R at a time: an item.  An item's work is its
+// visible blocks of 16 tokens (one scale each), TB blocks to a tile.  All
+// tiles of all items form one line (by sequence, head, row tile, tile), cut
+// into equal ranges, so that uneven contexts fill the GPU evenly; the lengths
+// are read on the device.
+#pragma once
+
+#include "tern_paged.cuh"
+
+namespace tern {
+
+constexpr int kMaxRows = 32;     // rows of an item, at most
+constexpr int kMaxCtas = 1024;   // CTAs of a launch (counters at the workspace's start)
+// A partial record: [rows][kPD] sums, then (m, z) of each row.
+__host__ __device__ constexpr int rec_floats(int rows) { return rows * (kPD + 2); }
+
+struct AttnParams {
+    PagedView v;
+    const float *q;
+    int ldq, Hq, GQ;
+    FastDiv by_gq;
+    int window, sinks;
+    float scale_log2;
+    float *out;
+    int ldo;
+    int *counters;
+    float *part;
+};
+
+// One sequence as this call sees it.
+struct Seq {
+    int start, rows;  // first row, rows x query heads of a group
+    int first;        // token of the first row
+    int end;          // tokens that may be read: min(ctx, page table)
+};
+
+__device__ __forceinline__ Seq sequence(const AttnParams &p, int b) {
+    const PagedView &v = p.v;
+    const int s0 = v.row_start[b], s1 = v.row_start[b + 1], ctx = v.ctx[b];
+    Seq s;
+    s.start = s0;
+    s.rows = s0 < 0 || s0 > v.T || s1 <= s0 ? 0 : (min(s1, v.T) - s0) * p.GQ;
+    s.first = ctx - (s1 - s0);
+    const long long cap = static_cast<long long>(v.pages_ld) * v.page_size;
+    s.end = static_cast<int>(min(static_cast<long long>(min(ctx, 0x7FFFFF00)), cap));
+    return s;
+}
+
+// Visible blocks of row tile rt: the k-th is block k below `sink`, else lo + k
+// - sink.
+struct Tiles {
+    int n, sink, lo;
+    __device__ __forceinline__ int block(int k) const { return k < sink ? k : lo + k - sink; }
+};
+
+template <int R>
+__device__ __forceinline__ Tiles tiles_of(const AttnParams &p, const Seq &s, int rt) {
+    const int r1 = min(R * rt + R, s.rows) - 1;
+    const int p0 = s.first + p.by_gq.quot(R * rt), p1 = s.first + p.by_gq.quot(r1);
+    const int hi = max(0, min(p1 + 1, s.end));
+    const int hit = (hi + kPB - 1) / kPB;
+    Tiles t;
+    t.lo = t.sink = 0;
+    if (p.window > 0) {
+        t.lo = min(max(0, p0 - p.window + 1) / kPB, hit);
+        t.sink = min((min(p.sinks, hi) + kPB - 1) / kPB, t.lo);
+    }
+    t.n = t.sink + hit - t.lo;
+    return t;
+}
+
+// Tiles of one KV head of a sequence (an item that sees nothing still counts
+// one: its rows are written as 0).
+template <int TB>
+__device__ __forceinline__ int tile_count(const Tiles &t) {
+    return max(1, (t.n + TB - 1) / TB);
+}
+template <int R, int TB>
+__device__ __forceinline__ long long head_units(const AttnParams &p, const Seq &s) {
+    long long u = 0;
+    for (int rt = 0; rt * R < s.rows; ++rt) u += tile_count<TB>(tiles_of<R>(p, s, rt));
+    return u;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Quotient of nonnegative numbers; 64-bit division is a long routine that
+// nearly every call can do without.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// The line of `total` tiles in n ranges: the first `more` hold base + 1 tiles,
+// the others base (n <= total, so none is empty).
+struct Ranges {
+    long long base, more;
+    __device__ __forceinline__ long long begin(int i) const { return base * i + min(static_cast<long long>(i), more); }
+    __device__ __forceinline__ int owner(long long u) const {
+        const long long big = more * (base + 1);
+        return static_cast<int>(u < big ? quot(u, base + 1) : more + quot(u - big, base));
+    }
+};
+
+// A place on the line: tile k of an item.
+template <int TB>
+struct Cursor {
+    int b, head, rt, k;
+    Seq s;
+    Tiles tl;
+    __device__ __forceinline__ int units() const { return tile_count<TB>(tl); }
+};
+
+template <int R, int TB, typename SeqOf>
+__device__ __forceinline__ void advance(const AttnParams &p, Cursor<TB> &x, int n, SeqOf seq_of) {
+    x.k += n;
+    while (x.k >= x.units()) {
+        x.k -= x.units();
+        if ((x.rt + 1) * R < x.s.rows) {
+            ++x.rt;
+        } else {
+            x.rt = 0;
+            if (++x.head == p.v.Hkv) {
+                x.head = 0;
+                do {
+                    if (++x.b >= p.v.B) return;  // past the line: the caller counts its tiles
+                    x.s = seq_of(x.b);
+                } while (x.s.rows == 0);
+            }
+        }
+        x.tl = tiles_of<R>(p, x.s, x.rt);
+    }
+}
+
+// The line of a launch, as a CTA of NT threads finds it.
+template <int NT>
+struct LineShared {
+    long long chunk[NT];  // line index where each thread's sequences begin
+    long long scan[NT / 32];
+    Seq seq[NT];          // the sequences, when each thread has one at most
+};
+struct Line {
+    long long total;
+    int per;  // sequences of a thread
+};
+
+template <int R, int TB, int NT>
+__device__ __forceinline__ Line make_line(const AttnParams &p, LineShared<NT> &S) {
+    const PagedView &v = p.v;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Line L;
+    L.per = (v.B + NT - 1) / NT;
+    long long mine = 0;
+    for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b) {
+        const Seq s = sequence(p, b);
+        mine += v.Hkv * head_units<R, TB>(p, s);
+        S.seq[tid] = s;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) S.scan[warp] = incl;
+    __syncthreads();
+    long long before = 0;
+    L.total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += S.scan[w];
+        L.total += S.scan[w];
+    }
+    S.chunk[tid] = before + incl - mine;
+    __syncthreads();
+    return L;
+}
+
+// The place of line index u < total (warp-collective).
+template <int R, int TB, int NT, typename SeqOf>
+__device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const LineShared<NT> &S, const Line &L, long long u,
+                                                 SeqOf seq_of) {
+    const int lane = threadIdx.x & 31;
+    Cursor<TB> cur;
+    int lo = 0;  // the last thread whose sequences begin at or before u
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        const unsigned le = __ballot_sync(0xffffffffu, S.chunk[32 * i + lane] <= u);
+        if (le) lo = 32 * i + 31 - __clz(le);
+    }
+    long long off = u - S.chunk[lo], ph;
+    int b = lo * L.per;
+    for (;; ++b) {
+        cur.s = seq_of(b);
+        ph = head_units<R, TB>(p, cur.s);
+        if (off < ph * p.v.Hkv) break;
+        off -= ph * p.v.Hkv;
+    }
+    cur.b = b;
+    cur.head = static_cast<int>(quot(off, ph));
+    off -= cur.head * ph;
+    cur.rt = 0;
+    cur.tl = tiles_of<R>(p, cur.s, 0);
+    while (off >= cur.units()) {
+        off -= cur.units();
+        cur.tl = tiles_of<R>(p, cur.s, ++cur.rt);
+    }
+    cur.k = static_cast<int>(off);
+    return cur;
+}
+
+// Row rr of an item to its place in out: four dimensions a lane.
+__device__ __forceinline__ void write_row(const AttnParams &p, int start, int head, int row, float4 o, float z, int d) {
+    const float iz = z > 0.0f ? 1.0f / z : 0.0f;
+    const int i = p.by_gq.quot(row);
+    *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(start + i) * p.ldo +
+                                (head * p.GQ + row - i * p.GQ) * kPD + d) =
+        make_float4(o.x * iz, o.y * iz, o.z * iz, o.w * iz);
+}
+
+__device__ __forceinline__ void add_scaled(float4 &o, float &z, float f, float4 x, float xz) {
+    z = fmaf(f, xz, z);
+    o.x = fmaf(f, x.x, o.x);
+    o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z);
+    o.w = fmaf(f, x.w, o.w);
+}
+
+// A piece of a cut item.
+struct Piece {
+    int valid, ends;   // ends: holds the item's last tile
+    int b, head, rt, units;
+    long long u0;      // line index of the item's first tile
+};
+
+// Items cut between CTAs: cut[0]: the CTA's range begins inside pc[0], whose
+// record lies in slot 2c; cut[1]: it ends inside pc[1] (slot 2c + 1; the
+// middle CTAs of an item have slot 2c alone).  Whoever finishes an item's last
+// part merges all of them in range order.  All threads of the CTA, after
+// their writes of the records; per_cta: ranges of the line in one CTA.
+template <int R, int NT, typename SeqOf>
+__device__ __forceinline__ void merge_cut_items(const AttnParams &p, const bool (&cut)[2], const Piece (&pc)[2],
+                                                const Ranges &ranges, int per_cta, int (&last)[2], SeqOf seq_of) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!cut[0] && !cut[1]) return;
+    __threadfence();
+    __syncthreads();
+    int first[2], parts[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        first[a] = parts[a] = 0;
+        if (!cut[a]) continue;
+        first[a] = ranges.owner(pc[a].u0) / per_cta;
+        parts[a] = ranges.owner(pc[a].u0 + pc[a].units - 1) / per_cta - first[a] + 1;
+        if (tid == 32 * a) {
+            const int done = atomicAdd(p.counters + first[a], 1);
+            last[a] = done + 1 == parts[a];
+            if (done + 1 == parts[a]) p.counters[first[a]] = 0;  // zero at rest
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        if (!cut[a] || !last[a]) continue;
+        __threadfence();
+        const Seq s = seq_of(pc[a].b);
+        for (int rr = warp; rr < R; rr += NT / 32) {
+            const int row = R * pc[a].rt + rr;
+            if (row >= s.rows) break;
+            auto record = [&](int i) {
+                return p.part + static_cast<int64_t>(2 * (first[a] + i) + (i == 0 ? 1 : 0)) * rec_floats(R);
+            };
+            float z = 0.0f, M = -INFINITY;
+            float4 o = make_float4(0, 0, 0, 0);
+            for (int i0 = 0; i0 < parts[a]; i0 += 16) {  // 16 parts at a time: their loads are all in flight at once
+                const int n = min(16, parts[a] - i0);
+                float2 mz = make_float2(-INFINITY, 0.0f);
+                if (lane < n) mz = __ldcg(reinterpret_cast<const float2 *>(record(i0 + lane) + R * kPD + 2 * rr));
+                float4 x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < n) x[i] = __ldcg(reinterpret_cast<const float4 *>(record(i0 + i) + rr * kPD + 4 * lane));
+                const float Mn = fmaxf(M, warp_max(mz.x));
+                const float ref = Mn == -INFINITY ? 0.0f : Mn;
+                const float back = ex2(M - ref);
+                z *= back;
+                o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
+                M = Mn;
+                const float f = ex2(mz.x - ref);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < n) add_scaled(o, z, __shfl_sync(0xffffffffu, f, i), x[i], __shfl_sync(0xffffffffu, mz.y, i));
+            }
+            write_row(p, s.start, pc[a].head, row, o, z, 4 * lane);
+        }
+    }
+}
+
+}  // namespace tern
