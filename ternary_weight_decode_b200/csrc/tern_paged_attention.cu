@@ -496,20 +496,21 @@ cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s
     p.counters = reinterpret_cast<int *>(A.workspace);
     p.part = A.workspace + kMaxCtas;
     CUtensorMap km, vm;
-    const uint64_t rows = static_cast<uint64_t>(A.cache.n_pages) * A.cache.Hkv * A.cache.page_size;
-    if (!make_u8_tmap_2d(&km, A.cache.k_codes, kPD, rows, kPD, kPD, kPB) ||
-        !make_u8_tmap_2d(&vm, A.cache.v_codes, kPD, rows, kPD, kPD, kPB)) {
+    const uint64_t cache_rows = static_cast<uint64_t>(A.cache.n_pages) * A.cache.Hkv * A.cache.page_size;
+    if (!make_u8_tmap_2d(&km, A.cache.k_codes, kPD, cache_rows, kPD, kPD, kPB) ||
+        !make_u8_tmap_2d(&vm, A.cache.v_codes, kPD, cache_rows, kPD, kPD, kPB)) {
         *why = "cuTensorMapEncodeTiled failed or is unavailable";
         return cudaErrorInvalidValue;
     }
-    // one CTA per SM, fewer when the tiles are few
-    const int64_t rowtiles = ceil_div(static_cast<int64_t>(std::min(A.batch.max_rows, A.batch.T)) * p.GQ, kRows);
     const int64_t span = A.window > 0 ? std::min<int64_t>(A.batch.max_ctx, static_cast<int64_t>(A.window) + A.sinks + 32)
                                       : A.batch.max_ctx;
-    const int64_t units = std::min<int64_t>(A.batch.B, A.batch.T) * A.cache.Hkv * rowtiles * ceil_div(span, kPB);
+    const int64_t rows = std::min<int64_t>(static_cast<int64_t>(std::min(A.batch.max_rows, A.batch.T)) * p.GQ, 1 << 30);
+    if (A.cache.kind == TERN_KV_INT8)
+        return launch_attention_tc(p, km, vm, static_cast<int>(rows), span, A.num_sms, s);
+    // one CTA per SM, fewer when the tiles are few
+    const int64_t units = std::min<int64_t>(A.batch.B, A.batch.T) * A.cache.Hkv * ceil_div(rows, kRows) * ceil_div(span, kPB);
     int64_t ctas = std::min<int64_t>(A.num_sms, ceil_div(units, kWarps));
     ctas = std::max<int64_t>(1, std::min<int64_t>(ctas, kMaxCtas));
-    if (A.cache.kind == TERN_KV_INT8) return launch_split<TERN_KV_INT8>(p, km, vm, static_cast<int>(ctas), s);
     return launch_split<TERN_KV_E4M3>(p, km, vm, static_cast<int>(ctas), s);
 }
 

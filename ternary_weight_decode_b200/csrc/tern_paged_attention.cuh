@@ -305,4 +305,10 @@ __device__ __forceinline__ void merge_cut_items(const AttnParams &p, const bool 
     }
 }
 
+// The int8 form on the 5th-generation tensor cores (tern_paged_attention_tc.cu):
+// max_rows: about the most rows (tokens times heads of a group) of a sequence,
+// span: about the most tokens one of them sees.
+cudaError_t launch_attention_tc(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int max_rows,
+                                int64_t span, int num_sms, cudaStream_t s);
+
 }  // namespace tern
