@@ -495,23 +495,27 @@ cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s
     p.ldo = A.ldo;
     p.counters = reinterpret_cast<int *>(A.workspace);
     p.part = A.workspace + kMaxCtas;
-    CUtensorMap km, vm;
+    CacheMaps maps;
     const uint64_t cache_rows = static_cast<uint64_t>(A.cache.n_pages) * A.cache.Hkv * A.cache.page_size;
-    if (!make_u8_tmap_2d(&km, A.cache.k_codes, kPD, cache_rows, kPD, kPD, kPB) ||
-        !make_u8_tmap_2d(&vm, A.cache.v_codes, kPD, cache_rows, kPD, kPD, kPB)) {
-        *why = "cuTensorMapEncodeTiled failed or is unavailable";
-        return cudaErrorInvalidValue;
+    // boxes of more blocks than the cache holds are never used, and not made
+    for (int i = 0; i < (A.cache.kind == TERN_KV_INT8 ? 4 : 1); ++i) {
+        const uint32_t box = static_cast<uint32_t>(std::min<uint64_t>(kPB << i, cache_rows));
+        if (!make_u8_tmap_2d(&maps.k[i], A.cache.k_codes, kPD, cache_rows, kPD, kPD, box) ||
+            !make_u8_tmap_2d(&maps.v[i], A.cache.v_codes, kPD, cache_rows, kPD, kPD, box)) {
+            *why = "cuTensorMapEncodeTiled failed or is unavailable";
+            return cudaErrorInvalidValue;
+        }
     }
     const int64_t span = A.window > 0 ? std::min<int64_t>(A.batch.max_ctx, static_cast<int64_t>(A.window) + A.sinks + 32)
                                       : A.batch.max_ctx;
     const int64_t rows = std::min<int64_t>(static_cast<int64_t>(std::min(A.batch.max_rows, A.batch.T)) * p.GQ, 1 << 30);
     if (A.cache.kind == TERN_KV_INT8)
-        return launch_attention_tc(p, km, vm, static_cast<int>(rows), span, A.num_sms, s);
+        return launch_attention_tc(p, maps, static_cast<int>(rows), span, A.num_sms, s);
     // one CTA per SM, fewer when the tiles are few
     const int64_t units = std::min<int64_t>(A.batch.B, A.batch.T) * A.cache.Hkv * ceil_div(rows, kRows) * ceil_div(span, kPB);
     int64_t ctas = std::min<int64_t>(A.num_sms, ceil_div(units, kWarps));
     ctas = std::max<int64_t>(1, std::min<int64_t>(ctas, kMaxCtas));
-    return launch_split<TERN_KV_E4M3>(p, km, vm, static_cast<int>(ctas), s);
+    return launch_split<TERN_KV_E4M3>(p, maps.k[0], maps.v[0], static_cast<int>(ctas), s);
 }
 
 }  // namespace tern

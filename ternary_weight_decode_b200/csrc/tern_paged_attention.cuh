@@ -19,6 +19,11 @@ constexpr int kMaxCtas = 1024;   // CTAs of a launch (counters at the workspace'
 // A partial record: [rows][kPD] sums, then (m, z) of each row.
 __host__ __device__ constexpr int rec_floats(int rows) { return rows * (kPD + 2); }
 
+// Tensor maps of the code arrays, boxes of 16 << i rows.
+struct CacheMaps {
+    CUtensorMap k[4], v[4];
+};
+
 struct AttnParams {
     PagedView v;
     const float *q;
@@ -115,6 +120,7 @@ struct Ranges {
 template <int TB>
 struct Cursor {
     int b, head, rt, k;
+    int ord;  // items passed since the range's first
     Seq s;
     Tiles tl;
     __device__ __forceinline__ int units() const { return tile_count<TB>(tl); }
@@ -125,6 +131,7 @@ __device__ __forceinline__ void advance(const AttnParams &p, Cursor<TB> &x, int 
     x.k += n;
     while (x.k >= x.units()) {
         x.k -= x.units();
+        ++x.ord;
         if ((x.rt + 1) * R < x.s.rows) {
             ++x.rt;
         } else {
@@ -215,6 +222,7 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
         cur.tl = tiles_of<R>(p, cur.s, ++cur.rt);
     }
     cur.k = static_cast<int>(off);
+    cur.ord = 0;
     return cur;
 }
 
@@ -308,7 +316,7 @@ __device__ __forceinline__ void merge_cut_items(const AttnParams &p, const bool 
 // The int8 form on the 5th-generation tensor cores (tern_paged_attention_tc.cu):
 // max_rows: about the most rows (tokens times heads of a group) of a sequence,
 // span: about the most tokens one of them sees.
-cudaError_t launch_attention_tc(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int max_rows,
-                                int64_t span, int num_sms, cudaStream_t s);
+cudaError_t launch_attention_tc(const AttnParams &p, const CacheMaps &maps, int max_rows, int64_t span, int num_sms,
+                                cudaStream_t s);
 
 }  // namespace tern

@@ -20,17 +20,22 @@
 // References: row r's weights are 2^(score - m_r) with m_r at least the largest
 // score so far; when a tile has a larger one (or block scales leave the
 // reference's range, or int32 could overflow), the sums are read, added to fp32
-// registers and begun again.  m_r is set four above the largest score, so that
-// happens a few times per item (28 of 32 bits remain; block scales may cost 8
+// registers and begun again.  m_r is set six above the largest score, so that
+// happens a few times per item (26 of 32 bits remain; block scales may cost 8
 // more).
 //
-// One CTA per SM; warps: 0 TMA and block look-up, 1 MMA issue, 2-3 query
-// digits, then one or two warpgroups of softmax (16 or 8 rows each; thread =
-// token of S, dimension of O).  A tile is eight visible blocks of 16 tokens of
-// an item, from anywhere in the sequence, so sinks and a window fill whole
-// tiles.  Everything runs ahead across items: TMA by the ring of stages, QK of
-// the next tile before PV of this one, the next item's digits while this one's
-// tiles are worked off.
+// One CTA per SM.  Warps of their own copy K and V, issue QK, issue PV and
+// make the query digits (issuing takes a thread some 450 cycles a product; one
+// warp for both took longer than a tile's bytes).  Two softmax groups (thread =
+// token of S, dimension of O; with 32 rows each group is two warpgroups of 16)
+// take the tiles in turn, each with its own accumulators, references and weight
+// buffer, so that one group's waits, fences and barriers pass under the other's
+// arithmetic; what they have of an item is put together at its end.  A tile is
+// eight visible blocks of 16 tokens of an item, from anywhere in the sequence,
+// so sinks and a window fill whole tiles.  Everything runs ahead across items:
+// K and V by rings of their own (a K stage is free after QK, a V stage after
+// PV), QK of the next tiles before PV of this one, the next item's digits while
+// this one's tiles are worked off.
 #include <algorithm>
 
 #include "tern_paged_attention.cuh"
@@ -43,23 +48,31 @@ namespace {
 constexpr int kTB = 8;                    // blocks of a tile
 constexpr int kTok = kTB * kPB;           // 128 tokens
 constexpr int kTileBytes = kTok * kPD;    // 16 KB of K or V codes
-constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kPBytes = kTok * 128;       // weight digits: a token's row of 128 bytes
-constexpr float kHeadroom = 4.0f;         // a new reference lies this far (log2) above the largest score
+constexpr int kInfo = 16;                 // tile infos kept: K's ring runs at most kStages + kSBufs + 2 tiles ahead of the softmax
+constexpr int kRowf = 8;                  // items whose score scales are kept (the digits run four ahead at most)
+constexpr float kHeadroom = 6.0f;         // a new reference lies this far (log2) above the largest score
 constexpr int kMaxChain = 256;            // tiles summed in int32: 256 * 128 * 255 * 127 < 2^31
 constexpr float kVRange = 1.0f / 256.0f;  // largest block scale of a tile, relative to the reference
 
 template <int R>
 struct Shape {
-    static constexpr int kWG = R > 8 ? 2 : 1;         // softmax warpgroups
-    static constexpr int kRW = R / kWG;               // rows of each
-    static constexpr int kThreads = 128 + 128 * kWG;
+    static constexpr int kHalves = R == 8 ? 1 : 2;    // warpgroups of a softmax group
+    static constexpr int kRW = R / kHalves;           // rows of each
+    static constexpr int kHelpers = R == 8 ? 8 : 4;   // warps in front of the softmax warps
+    static constexpr int kThreads = 32 * kHelpers + 2 * kHalves * 128;
+    static constexpr int kGroup = 128 * kHalves;      // threads of a softmax group
+    // warps: copies of K (of K and V with 4 helpers), of V, issue of QK, of PV, query digits
+    static constexpr int kWarpK = 0, kWarpV = R == 8 ? 1 : -1, kWarpQK = R == 8 ? 2 : 1, kWarpPV = R == 8 ? 3 : 2,
+                         kWarpQ = R == 8 ? 4 : 3;
+    static constexpr int kSBufs = R == 8 ? 4 : 2;     // S accumulators
     static constexpr int kNS = R == 8 ? 32 : 3 * R;   // columns of S: 3 per row, a multiple of 16
-    static constexpr int kNP = 4 * R;                 // columns of O
-    static constexpr int kStages = R > 8 ? 4 : 5;
+    static constexpr int kNP = 4 * R;                 // columns of O: the bytes of a token's row of weight digits
+    static constexpr int kStages = R == 8 ? 6 : 4;    // of K and of V
     static constexpr int kQBytes = kNS * 128;
-    static constexpr uint32_t kTmemCols = 2 * kNS + kNP <= 128 ? 128 : 512;
-    static constexpr uint32_t kO = 2 * kNS;           // first column of O
+    static constexpr int kPBytes = kTok * kNP;        // (also holds a group's R x 128 sums at the end of an item)
+    static constexpr uint32_t kTmemCols = R == 8 ? 256 : 512;
+    static constexpr uint32_t kO = kSBufs * kNS;      // first column of O
+    static_assert(kSBufs * kNS + 2 * kNP <= kTmemCols, "tensor memory");
 };
 
 // One tile, as the softmax and MMA warps see it.
@@ -67,22 +80,34 @@ struct TileInfo {
     float ks[kTB], vs[kTB];
     int j0[kTB];      // first token of each block
     int valid;        // bit j: block j is there
-    int flags;        // kFirst, kLast, kEdge, kEnds
+    int flags;
     float vmax;       // largest value scale
-    int b, head, rt, k, units;
+    int b, head, rt, k, units, ord;
 };
-constexpr int kFirst = 1, kLast = 2, kEdge = 4, kEnds = 8;  // first / last tile of the item here, masks needed, item's end
+enum : int {
+    kFirst = 1,       // the first tile of its item in this CTA
+    kLast = 2,        // the last
+    kGroupFirst = 4,  // the first of its item that its group has here
+    kGroupLast = 8,   // the last
+    kBoth = 16,       // both groups have tiles of the item
+    kEdge = 32,       // masks needed
+    kEnds = 64,       // the item's last tile
+};
 
 template <int R>
 struct TcShared {
     using Sh = Shape<R>;
-    TileInfo info[Sh::kStages];
-    float rowf[2][R];                 // score scale of each row's digits
-    float wmax[Sh::kWG][4][Sh::kRW];
-    float zsum[Sh::kWG][4][Sh::kRW];
+    TileInfo info[kInfo];
+    float4 rowf[kRowf][R / 4];        // score scale of each row's digits
+    float4 m[2][R / 4], mref[2][R / 4];  // each group's references; mref: 0 for a row that has seen nothing
+    float4 back[2][R / 4];            // what new references make of the sums before
+    float wmax[2][4][R];
+    float zsum[2][4][R];
+    float4 sum_m[2][R / 4];           // a group's references and sums when it hands its part of an item over
+    float sum_z[2][R];
     LineShared<Sh::kThreads> line;
-    uint64_t kv_full[Sh::kStages], kv_empty[Sh::kStages];
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], q_full[2], q_empty[2];
+    uint64_t k_full[Sh::kStages], k_empty[Sh::kStages], v_full[Sh::kStages], v_empty[Sh::kStages];
+    uint64_t s_full[Sh::kSBufs], s_empty[Sh::kSBufs], p_full[2], p_empty[2], q_full[2], q_empty[2], sum_full[2], sum_empty[2];
     Piece piece[2];
     uint32_t tmem;
     int accumulate[2];
@@ -92,9 +117,24 @@ struct TcShared {
 template <int R>
 constexpr size_t tc_smem() {
     using Sh = Shape<R>;
-    return Sh::kStages * kStageBytes + 2 * kPBytes + 2 * Sh::kQBytes + sizeof(TcShared<R>) + 1024;
+    return 2 * Sh::kStages * kTileBytes + 2 * Sh::kPBytes + 2 * Sh::kQBytes + sizeof(TcShared<R>) + 1024;
 }
 static_assert(tc_smem<8>() <= 227 * 1024 && tc_smem<32>() <= 227 * 1024, "shared memory of one CTA");
+
+// B operand descriptor of the weight digits, N-major: a token's row of kNP
+// bytes, 128 (128-byte swizzle, layout 2) or 32 (32-byte swizzle, layout 6:
+// 16-byte chunk c of row k stored at c ^ (k / 4 % 2)), groups of 8 tokens 8 rows apart.
+template <int R>
+__device__ __forceinline__ uint64_t weights_desc(uint32_t saddr) {
+    if constexpr (R == 8)
+        return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(256u >> 4) << 32) |
+               (1ull << 46) | (6ull << 61);
+    return smem_desc_sw128(saddr);
+}
+template <int R>
+__device__ __forceinline__ int weights_chunk(int c, int k) {
+    return R == 8 ? c ^ (k >> 2 & 1) : c ^ (k & 7);
+}
 
 // A wait of this thread; once one has run out, none of the later ones waits.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
@@ -118,55 +158,210 @@ __device__ __forceinline__ float redux_max(float x) {
     return y;
 }
 
+// Barrier over the N threads of softmax group g, with the "or" of x.
 template <int N>
-__device__ __forceinline__ bool any_of(bool x) {  // named barrier 1 over the N softmax threads
+__device__ __forceinline__ bool any_of(bool x, int g) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(x)), "n"(N)
+        : "r"(static_cast<uint32_t>(x)), "r"(1 + g), "n"(N)
         : "memory");
     return r != 0;
 }
 
+// Sums of each z[r] over the warp; lane l ends up with that of row l % R.
+template <int R>
+__device__ __forceinline__ float sum_rows(float (&z)[R], int lane) {
+#pragma unroll
+    for (int h = R / 2; h >= 1; h >>= 1) {
+        const bool up = (lane & h) != 0;
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? z[j] : z[j + h], h);
+            z[j] = (up ? z[j + h] : z[j]) + other;
+        }
+    }
+#pragma unroll
+    for (int h = R; h < 32; h <<= 1) z[0] += __shfl_xor_sync(0xffffffffu, z[0], h);
+    return z[0];
+}
+
+// Adds what PV has summed to o: digits of value 2^(8 k - 32), times the value
+// reference.
+template <int RW>
+__device__ __forceinline__ void add_sums(uint32_t taddr, float vref, float (&o)[RW]) {
+#pragma unroll
+    for (int h = 0; h < RW / 8; ++h) {
+        uint32_t ov[32];
+        tmem_ld32(taddr + 32 * h, ov);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float t = static_cast<float>(static_cast<int>(ov[4 * e])) * 0x1p-32f;
+            t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 1])), 0x1p-24f, t);
+            t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 2])), 0x1p-16f, t);
+            t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 3])), 0x1p-8f, t);
+            o[8 * h + e] = fmaf(t, vref, o[8 * h + e]);
+        }
+    }
+}
+
+// The copies of K's or V's blocks, or of both, of a range's tiles; K's also
+// writes the tiles' infos.
+template <int R, bool IS_K, bool IS_V, typename SeqOf>
+__device__ __forceinline__ void copy_blocks(const AttnParams &p, const CacheMaps &maps, TcShared<R> &S, uint8_t *kring,
+                                            uint8_t *vring, const Line &L, long long u0, int count, SeqOf seq_of) {
+    constexpr int kSt = Shape<R>::kStages;
+    const PagedView &v = p.v;
+    const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
+    bool ok = true;
+    // blocks of the tiles, four tiles at a time (lane = 8 * tile + block)
+    Cursor<kTB> cur = find_place<R, kTB>(p, S.line, L, u0, seq_of), at = cur;
+    if (sub < count) advance<R>(p, cur, sub, seq_of);
+    int bi = -1, j0 = 0;
+    float ks = 0.0f, vs = 0.0f;
+    auto look_up = [&](int i0) {  // this lane's block of tile i0 + sub
+        bi = -1;
+        ks = vs = 0.0f;
+        if (i0 + sub >= count) return;
+        at = cur;
+        const int kb = kTB * cur.k + j;
+        if (kb < cur.tl.n) {
+            const int blk = cur.tl.block(kb);
+            j0 = blk * kPB;
+            const int64_t x = block_index(v, cur.b, blk);
+            if (x >= 0) {
+                bi = static_cast<int>(x) + cur.head * v.bpp;
+                if (IS_K) {
+                    ks = v.ks[bi];
+                    vs = v.vs[bi];
+                }
+            }
+        }
+        if (i0 + 4 + sub < count) advance<R>(p, cur, 4, seq_of);
+    };
+    look_up(0);
+    for (int i0 = 0; i0 < count; i0 += 4) {
+        const int b_now = bi, j0_now = j0;
+        const float ks_now = ks, vs_now = vs;
+        const Cursor<kTB> it = at;
+        const unsigned there = __ballot_sync(0xffffffffu, b_now >= 0);
+        // runs of blocks that lie behind one another in the cache: one copy each for 8, 4, 2 or 1 of them
+        // (a copy of 16 rows takes as long as one of 64: 2150 cycles a tile in single blocks, 1690 in 64 rows)
+        const int before = __shfl_up_sync(0xffffffffu, b_now, 1);
+        const unsigned follows = __ballot_sync(0xffffffffu, b_now >= 0 && b_now == before + 1) >> (8 * sub);
+        int size = 0;  // log2 of the blocks this lane copies, -1: another lane does
+        if ((follows & 0xFEu) == 0xFEu) size = 3;
+        else if ((follows >> (j & 4) & 0xEu) == 0xEu) size = 2;
+        else if (follows >> (j & 6) & 2u) size = 1;
+        if (b_now < 0 || (j & ((1 << size) - 1))) size = -1;
+        unsigned not_whole = 0;
+        float vmax = 0.0f;
+        if (IS_K) {
+            // masks: a block whose tokens not every row sees, or that is missing
+            const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
+            const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
+            const bool whole = b_now >= 0 && j0_now + kPB - 1 <= p_min &&
+                               (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
+            not_whole = __ballot_sync(0xffffffffu, !whole);
+            vmax = vs_now;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+        }
+        if (i0 + 4 < count) look_up(i0 + 4);  // in flight while the stages come free
+        for (int e = 0; e < 4 && i0 + e < count; ++e) {
+            const int i = i0 + e, stage = i % kSt;
+            if (IS_K) wait(&S.k_empty[stage], ((i / kSt) + 1) & 1, ok);
+            if (IS_K && sub == e) {
+                TileInfo &f = S.info[i % kInfo];
+                f.ks[j] = ks_now;
+                f.vs[j] = vs_now;
+                f.j0[j] = j0_now;
+                if (j == 0) {
+                    const int since = min(it.k, i), left = min(it.units() - 1 - it.k, count - 1 - i);
+                    f.valid = there >> (8 * e) & 255;
+                    f.flags = (since == 0 ? kFirst : 0) | (left == 0 ? kLast : 0) | (since < 2 ? kGroupFirst : 0) |
+                              (left < 2 ? kGroupLast : 0) | (since + left > 0 ? kBoth : 0) |
+                              ((not_whole >> (8 * e) & 255) ? kEdge : 0) | (it.k + 1 == it.units() ? kEnds : 0);
+                    f.vmax = vmax;
+                    f.b = it.b;
+                    f.head = it.head;
+                    f.rt = it.rt;
+                    f.k = it.k;
+                    f.units = it.units();
+                    f.ord = it.ord;
+                }
+            }
+            const uint32_t bytes = __popc(there >> (8 * e) & 255) * kPB * kPD;
+            const int at_stage = stage * kTileBytes + j * kPB * kPD;
+            if (IS_K) {
+                __syncwarp();
+                if (lane == 8 * e) mbar_arrive_expect_tx(&S.k_full[stage], bytes);
+                __syncwarp();
+                if (sub == e && size >= 0) tma_load_2d_nohint(kring + at_stage, &maps.k[size], 0, b_now * kPB, &S.k_full[stage]);
+            }
+            if (IS_V) {
+                wait(&S.v_empty[stage], ((i / kSt) + 1) & 1, ok);
+                if (lane == 8 * e) mbar_arrive_expect_tx(&S.v_full[stage], bytes);
+                __syncwarp();
+                if (sub == e && size >= 0) tma_load_2d_nohint(vring + at_stage, &maps.v[size], 0, b_now * kPB, &S.v_full[stage]);
+            }
+        }
+    }
+    // no copy is in flight when the CTA ends, even after a wait that ran out
+    bool land = true;
+    for (int i = max(0, count - kSt); i < count; ++i) {
+        if (IS_K) wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
+        if (IS_V) wait(&S.v_full[i % kSt], (i / kSt) & 1, land);
+    }
+}
+
 template <int R>
 __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
-    attn_tc_paged_kernel(AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap) {
+    attn_tc_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps) {
     using Sh = Shape<R>;
-    constexpr int kSt = Sh::kStages, kNT = Sh::kThreads, kSoft = 128 * Sh::kWG, kRW = Sh::kRW;
+    constexpr int kSt = Sh::kStages, kRW = Sh::kRW, kGroup = Sh::kGroup;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *kv = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *pbuf = kv + kSt * kStageBytes;
-    uint8_t *qbuf = pbuf + 2 * kPBytes;
+    uint8_t *kring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *vring = kring + kSt * kTileBytes;
+    uint8_t *pbuf = vring + kSt * kTileBytes;
+    uint8_t *qbuf = pbuf + 2 * Sh::kPBytes;
     TcShared<R> &S = *reinterpret_cast<TcShared<R> *>(qbuf + 2 * Sh::kQBytes);
-    const PagedView &v = p.v;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = blockIdx.x;
     bool ok = true;
 
     if (tid == 0) {
-        prefetch_tmap(&kmap);
-        prefetch_tmap(&vmap);
+        for (int i = 0; i < 4; ++i) {
+            prefetch_tmap(&maps.k[i]);
+            prefetch_tmap(&maps.v[i]);
+        }
         for (int i = 0; i < kSt; ++i) {
-            mbar_init(&S.kv_full[i], 1);
-            mbar_init(&S.kv_empty[i], 1);
+            mbar_init(&S.k_full[i], 1);
+            mbar_init(&S.k_empty[i], 1);
+            mbar_init(&S.v_full[i], 1);
+            mbar_init(&S.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&S.s_full[i], 1);
-            mbar_init(&S.s_empty[i], 4 * Sh::kWG);
-            mbar_init(&S.p_full[i], 4 * Sh::kWG);
+            mbar_init(&S.p_full[i], 4 * Sh::kHalves);
             mbar_init(&S.p_empty[i], 1);
-            mbar_init(&S.q_full[i], 2);
-            mbar_init(&S.q_empty[i], 1 + 4 * Sh::kWG);
+            mbar_init(&S.q_full[i], 1);
+            mbar_init(&S.q_empty[i], 1);
+            mbar_init(&S.sum_full[i], 4 * Sh::kHalves);
+            mbar_init(&S.sum_empty[i], 4 * Sh::kHalves);
             S.piece[i].valid = 0;
+        }
+        for (int i = 0; i < Sh::kSBufs; ++i) {
+            mbar_init(&S.s_full[i], 2);
+            mbar_init(&S.s_empty[i], 4 * Sh::kHalves);
         }
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == Sh::kWarpQK) {
         tmem_alloc(&S.tmem, Sh::kTmemCols);
         tmem_relinquish();
     }
@@ -185,130 +380,65 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
     const int count = c < G ? static_cast<int>(ranges.begin(c + 1) - u0) : 0;
     const uint32_t tmem = S.tmem;
 
-    if (warp == 0 && count > 0) {
-        // ---- blocks of the tiles, four tiles at a time (lane = 8 * tile + block), and their copies
-        Cursor<kTB> cur = find_place<R, kTB>(p, S.line, L, u0, seq_of);
-        const int sub = lane >> 3, j = lane & 7;
-        if (sub < count) advance<R>(p, cur, sub, seq_of);
-        int bi = -1, j0 = 0;
-        float ks = 0.0f, vs = 0.0f;
-        Cursor<kTB> at = cur;
-        auto look_up = [&](int i0) {  // this lane's block of tile i0 + sub
-            bi = -1;
-            ks = vs = 0.0f;
-            if (i0 + sub >= count) return;
-            at = cur;
-            const int kb = kTB * cur.k + j;
-            if (kb < cur.tl.n) {
-                const int blk = cur.tl.block(kb);
-                j0 = blk * kPB;
-                const int64_t x = block_index(v, cur.b, blk);
-                if (x >= 0) {
-                    bi = static_cast<int>(x) + cur.head * v.bpp;
-                    ks = v.ks[bi];
-                    vs = v.vs[bi];
-                }
-            }
-            if (i0 + 4 + sub < count) advance<R>(p, cur, 4, seq_of);
-        };
-        look_up(0);
-        for (int i0 = 0; i0 < count; i0 += 4) {
-            const int b_now = bi, j0_now = j0;
-            const float ks_now = ks, vs_now = vs;
-            const Cursor<kTB> it = at;
-            // masks: a block whose tokens not every row sees, or that is missing
-            const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
-            const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
-            const bool whole = b_now >= 0 && j0_now + kPB - 1 <= p_min &&
-                               (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
-            const unsigned not_whole = __ballot_sync(0xffffffffu, !whole);
-            const unsigned there = __ballot_sync(0xffffffffu, b_now >= 0);
-            float vmax = vs_now;
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-            if (i0 + 4 < count) look_up(i0 + 4);  // in flight while the stages come free
-            for (int e = 0; e < 4 && i0 + e < count; ++e) {
-                const int i = i0 + e, stage = i % kSt;
-                wait(&S.kv_empty[stage], ((i / kSt) + 1) & 1, ok);
-                TileInfo &f = S.info[stage];
-                if (sub == e) {
-                    f.ks[j] = ks_now;
-                    f.vs[j] = vs_now;
-                    f.j0[j] = j0_now;
-                    if (j == 0) {
-                        f.valid = there >> (8 * e) & 255;
-                        f.flags = (i == 0 || it.k == 0 ? kFirst : 0) | (it.k + 1 == it.units() ? kEnds | kLast : 0) |
-                                  (i + 1 == count ? kLast : 0) | ((not_whole >> (8 * e) & 255) ? kEdge : 0);
-                        f.vmax = vmax;
-                        f.b = it.b;
-                        f.head = it.head;
-                        f.rt = it.rt;
-                        f.k = it.k;
-                        f.units = it.units();
-                    }
-                }
-                __syncwarp();
-                if (lane == 8 * e)
-                    mbar_arrive_expect_tx(&S.kv_full[stage], __popc(there >> (8 * e) & 255) * 2 * kPB * kPD);
-                __syncwarp();
-                if (sub == e && b_now >= 0) {
-                    uint8_t *dst = kv + stage * kStageBytes + j * kPB * kPD;
-                    tma_load_2d_nohint(dst, &kmap, 0, b_now * kPB, &S.kv_full[stage]);
-                    tma_load_2d_nohint(dst + kTileBytes, &vmap, 0, b_now * kPB, &S.kv_full[stage]);
-                }
-            }
-        }
-        // no copy is in flight when the CTA ends, even after a wait that ran out
-        bool land = true;
-        for (int i = max(0, count - kSt); i < count; ++i) wait(&S.kv_full[i % kSt], (i / kSt) & 1, land);
-    } else if (warp == 1 && count > 0) {
-        // ---- matrix products: QK of tile i + 1 before PV of tile i
+    if (count == 0) {
+    } else if (warp == Sh::kWarpK) {
+        copy_blocks<R, true, Sh::kWarpV < 0>(p, maps, S, kring, vring, L, u0, count, seq_of);
+    } else if (warp == Sh::kWarpV) {
+        copy_blocks<R, false, true>(p, maps, S, kring, vring, L, u0, count, seq_of);
+    } else if (warp == Sh::kWarpQK) {
+        // ---- S of each tile, as soon as its keys are there and its accumulator has been read
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_i8(128, Sh::kNS, 1, 1);
-            constexpr uint32_t id_o = idesc_i8(128, Sh::kNP, 1, 0) | (1u << 15) | (1u << 16);  // both operands M/N-major
             int item = -1;
-            auto qk = [&](int i) {
-                const int stage = i % kSt;
-                wait(&S.kv_full[stage], (i / kSt) & 1, ok);
-                const int flags = S.info[stage].flags;
+            for (int i = 0; i < count; ++i) {
+                const int stage = i % kSt, buf = i % Sh::kSBufs;
+                wait(&S.k_full[stage], (i / kSt) & 1, ok);
+                const int flags = S.info[i % kInfo].flags;
                 if (flags & kFirst) {
                     ++item;
                     wait(&S.q_full[item & 1], (item >> 1) & 1, ok);
                 }
-                wait(&S.s_empty[i & 1], ((i >> 1) + 1) & 1, ok);
+                wait(&S.s_empty[buf], ((i / Sh::kSBufs) + 1) & 1, ok);
                 tc_fence_after_sync();
-                const uint32_t a = smem_u32(kv + stage * kStageBytes), b = smem_u32(qbuf + (item & 1) * Sh::kQBytes);
+                const uint32_t a = smem_u32(kring + stage * kTileBytes), b = smem_u32(qbuf + (item & 1) * Sh::kQBytes);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_i8_ss(tmem + (i & 1) * Sh::kNS, smem_desc_sw128(a + 32 * k), smem_desc_sw128(b + 32 * k), id_s, k > 0);
-                tc_commit(&S.s_full[i & 1]);
+                    mma_i8_ss(tmem + buf * Sh::kNS, smem_desc_sw128(a + 32 * k), smem_desc_sw128(b + 32 * k), id_s, k > 0);
+                tc_commit(&S.s_full[buf]);
+                tc_commit(&S.k_empty[stage]);
                 if (flags & kLast) tc_commit(&S.q_empty[item & 1]);
-            };
-            qk(0);
-            for (int i = 0; i < count; ++i) {
-                if (i + 1 < count) qk(i + 1);
-                const int stage = i % kSt;
-                wait(&S.p_full[i & 1], (i >> 1) & 1, ok);
-                tc_fence_after_sync();
-                const uint32_t a = smem_u32(kv + stage * kStageBytes + kTileBytes), b = smem_u32(pbuf + (i & 1) * kPBytes);
-                const uint32_t acc = S.accumulate[i & 1];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_i8_ss(tmem + Sh::kO, smem_desc_sw128(a + 4096 * k), smem_desc_sw128(b + 4096 * k), id_o,
-                              k > 0 || acc);
-                tc_commit(&S.kv_empty[stage]);
-                tc_commit(&S.p_empty[i & 1]);
+                mbar_arrive(&S.s_full[buf]);  // (hands on the tile's info and the rows' scales, which this thread has acquired)
             }
         }
         __syncwarp();
-    } else if (warp < 4 && count > 0) {
-        // ---- query digits of each item, ahead of its tiles; warp 2 the even rows, warp 3 the odd ones
+    } else if (warp == Sh::kWarpPV) {
+        // ---- O of each tile, added to its group's sums
+        if (lane == 0) {
+            constexpr uint32_t id_o = idesc_i8(128, Sh::kNP, 1, 0) | (1u << 15) | (1u << 16);  // both operands M/N-major
+            for (int i = 0; i < count; ++i) {
+                const int stage = i % kSt, g = i & 1;
+                wait(&S.v_full[stage], (i / kSt) & 1, ok);
+                wait(&S.p_full[g], (i >> 1) & 1, ok);
+                tc_fence_after_sync();
+                const uint32_t a = smem_u32(vring + stage * kTileBytes), b = smem_u32(pbuf + g * Sh::kPBytes);
+                const uint32_t acc = S.accumulate[g];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_i8_ss(tmem + Sh::kO + g * Sh::kNP, smem_desc_sw128(a + 4096 * k),
+                              weights_desc<R>(b + 32 * Sh::kNP * k), id_o, k > 0 || acc);
+                tc_commit(&S.p_empty[g]);
+                tc_commit(&S.v_empty[stage]);
+            }
+        }
+        __syncwarp();
+    } else if (warp == Sh::kWarpQ) {
+        // ---- query digits of each item, ahead of its tiles
         Cursor<kTB> cur = find_place<R, kTB>(p, S.line, L, u0, seq_of);
         for (int done = 0, item = 0; done < count; ++item) {
             wait(&S.q_empty[item & 1], ((item >> 1) + 1) & 1, ok);
             uint8_t *qb = qbuf + (item & 1) * Sh::kQBytes;
-#pragma unroll 4
-            for (int rr = warp - 2; rr < R; rr += 2) {
+#pragma unroll 8
+            for (int rr = 0; rr < R; ++rr) {
                 const int row = R * cur.rt + rr;
                 float4 x = make_float4(0, 0, 0, 0);
                 if (row < cur.s.rows) {
@@ -335,7 +465,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                 for (int k = 0; k < 3; ++k)
                     *reinterpret_cast<uint32_t *>(qb + sw128_offset(6 * (rr >> 1) + 2 * k + (rr & 1), 4 * lane)) = w[k];
                 if (lane == 0)
-                    S.rowf[item & 1][rr] =
+                    reinterpret_cast<float *>(S.rowf[item % kRowf])[rr] =
                         row < cur.s.rows ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.0f;
             }
             fence_proxy_async_smem();
@@ -345,56 +475,62 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             done += n;
             if (done < count) advance<R>(p, cur, n, seq_of);
         }
-    } else if (count > 0) {
-        // ---- softmax: thread = token of the tile and dimension of the output
-        const int wg = (warp - 4) >> 2, w4 = warp & 3, me = tid & 127;
+    } else if (warp >= Sh::kHelpers) {
+        // ---- softmax group g: tiles g, g + 2, ...; thread = token of the tile and dimension of the output, rows
+        // r0 .. r0 + kRW - 1
+        const int in = tid - 32 * Sh::kHelpers, g = in / kGroup, gt = in % kGroup, w4 = warp & 3, me = tid & 127;
+        const int r0 = kRW * (gt >> 7);
         const uint32_t lanes = static_cast<uint32_t>(w4) << 21;  // this warp's quarter of tensor memory
-        float m[kRW], z[kRW], o[kRW], rowf[kRW];
+        const uint32_t ts = tmem + lanes + 3 * r0, to = tmem + lanes + Sh::kO + g * Sh::kNP + 4 * r0;
+        uint8_t *my_p = pbuf + g * Sh::kPBytes;
+        float z[kRW], o[kRW];
         float vref = 1.0f, inv_vref = 1.0f;
-        int chain = 0, item = -1, k_first = 0;
-        for (int i = 0; i < count; ++i) {
-            const int stage = i % kSt;
-            const TileInfo &f = S.info[stage];
-            wait(&S.kv_full[stage], (i / kSt) & 1, ok);  // the tile's info
-            wait(&S.s_full[i & 1], (i >> 1) & 1, ok);
+        int chain = 0, k_first = 0;
+        int given = 0, taken = 0;  // items handed to the other group, and taken from it
+        for (int i = g; i < count; i += 2) {
+            const TileInfo &f = S.info[i % kInfo];
+            const int buf = i % Sh::kSBufs;
+            wait(&S.s_full[buf], (i / Sh::kSBufs) & 1, ok);
             tc_fence_after_sync();
             const int flags = f.flags;
-            if (flags & kFirst) {
-                ++item;
-                k_first = f.k;
+            if (flags & kGroupFirst) {
+                k_first = f.k - ((flags & kFirst) ? 0 : 1);  // the first tile that the CTA has of the item
 #pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    rowf[r] = S.rowf[item & 1][kRW * wg + r];
-                    m[r] = -INFINITY;
-                    z[r] = o[r] = 0.0f;
+                for (int r = 0; r < kRW; ++r) z[r] = o[r] = 0.0f;
+                if (gt < R) {
+                    reinterpret_cast<float *>(S.m[g])[gt] = -INFINITY;
+                    reinterpret_cast<float *>(S.mref[g])[gt] = 0.0f;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.q_empty[item & 1]);
+                any_of<kGroup>(false, g);
             }
-            // scores of this token: x[r], in log2
+            // scores of this token, in log2
             float x[kRW];
             {
-                uint32_t sv[3 * kRW];
-                const uint32_t a = tmem + lanes + (i & 1) * Sh::kNS + 3 * kRW * wg;
+                const float ks = f.ks[me >> 4];
+                const float2 up = make_float2(256.0f, 256.0f), ks2 = make_float2(ks, ks);
 #pragma unroll
-                for (int h = 0; h < 3 * kRW / 8; ++h) tmem_ld8(a + 8 * h, *reinterpret_cast<uint32_t(*)[8]>(sv + 8 * h));
-                tmem_wait_ld();
+                for (int h = 0; h < kRW / 8; ++h) {
+                    uint32_t sv[24];
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) tmem_ld8(ts + buf * Sh::kNS + 24 * h + 8 * e, *reinterpret_cast<uint32_t(*)[8]>(sv + 8 * e));
+                    tmem_wait_ld();
+                    const float4 ra = S.rowf[f.ord % kRowf][r0 / 4 + 2 * h], rb = S.rowf[f.ord % kRowf][r0 / 4 + 2 * h + 1];
+                    const float2 rf[4] = {make_float2(ra.x, ra.y), make_float2(ra.z, ra.w), make_float2(rb.x, rb.y),
+                                          make_float2(rb.z, rb.w)};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t *d = sv + 6 * r;
+                        const float2 d0 = make_float2(small_int(d[0]), small_int(d[1]));
+                        const float2 d1 = make_float2(small_int(d[2]), small_int(d[3]));
+                        const float2 d2 = make_float2(small_int(d[4]), small_int(d[5]));
+                        const float2 s2 = __fmul2_rn(__ffma2_rn(__ffma2_rn(d2, up, d1), up, d0), __fmul2_rn(rf[r], ks2));
+                        x[8 * h + 2 * r] = s2.x;
+                        x[8 * h + 2 * r + 1] = s2.y;
+                    }
+                }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&S.s_empty[i & 1]);
-                const float ks = f.ks[me >> 4];
-#pragma unroll
-                for (int r = 0; r < kRW; r += 2) {
-                    const uint32_t *d = sv + 3 * r;
-                    const float2 d0 = make_float2(small_int(d[0]), small_int(d[1]));
-                    const float2 d1 = make_float2(small_int(d[2]), small_int(d[3]));
-                    const float2 d2 = make_float2(small_int(d[4]), small_int(d[5]));
-                    const float2 up = make_float2(256.0f, 256.0f);
-                    const float2 s2 = __fmul2_rn(__ffma2_rn(__ffma2_rn(d2, up, d1), up, d0),
-                                                 __fmul2_rn(make_float2(rowf[r], rowf[r + 1]), make_float2(ks, ks)));
-                    x[r] = s2.x;
-                    x[r + 1] = s2.y;
-                }
+                if (lane == 0) mbar_arrive(&S.s_empty[buf]);
             }
             if (flags & kEdge) {
                 const Seq s = seq_of(f.b);
@@ -402,51 +538,52 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                 const bool there = f.valid >> (me >> 4) & 1;
 #pragma unroll
                 for (int r = 0; r < kRW; ++r) {
-                    const int pos = s.first + p.by_gq.quot(min(R * f.rt + kRW * wg + r, s.rows - 1));
+                    const int pos = s.first + p.by_gq.quot(min(R * f.rt + r0 + r, s.rows - 1));
                     if (!there || tok > pos || (p.window > 0 && tok <= pos - p.window && tok >= p.sinks)) x[r] = -INFINITY;
                 }
             }
             const float vmax = f.vmax;
-            bool flush = (flags & kFirst) || chain >= kMaxChain || vmax > vref || (vmax > 0.0f && vmax < vref * kVRange);
+            bool flush = (flags & kGroupFirst) || chain >= kMaxChain || vmax > vref || (vmax > 0.0f && vmax < vref * kVRange);
 #pragma unroll
-            for (int r = 0; r < kRW; ++r) flush |= x[r] > m[r];
-            if (any_of<kSoft>(flush)) {
+            for (int h = 0; h < kRW / 4; ++h) {
+                const float4 m = S.m[g][r0 / 4 + h];
+                flush |= x[4 * h] > m.x || x[4 * h + 1] > m.y || x[4 * h + 2] > m.z || x[4 * h + 3] > m.w;
+            }
+            if (any_of<kGroup>(flush, g)) {
                 // ---- new references: each row's largest score of the tile over all 128 tokens
 #pragma unroll
                 for (int r = 0; r < kRW; ++r) {
                     const float y = redux_max(x[r]);
-                    if (lane == 0) S.wmax[wg][w4][r] = y;
+                    if (lane == 0) S.wmax[g][w4][r0 + r] = y;
                 }
-                if (!(flags & kFirst)) {
-                    // what PV of the tiles before has summed: digits o_k of value 2^(8 k - 32), in units of the references
-                    wait(&S.p_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, ok);
+                if (chain > 0) {
+                    wait(&S.p_empty[g], ((i - 2) >> 1) & 1, ok);  // PV of this group's last tile
                     tc_fence_after_sync();
-#pragma unroll
-                    for (int h = 0; h < kRW / 2; ++h) {
-                        uint32_t ov[8];
-                        tmem_ld8(tmem + lanes + Sh::kO + 4 * kRW * wg + 8 * h, ov);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float t = static_cast<float>(static_cast<int>(ov[4 * e])) * 0x1p-32f;
-                            t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 1])), 0x1p-24f, t);
-                            t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 2])), 0x1p-16f, t);
-                            t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 3])), 0x1p-8f, t);
-                            o[2 * h + e] = fmaf(t, vref, o[2 * h + e]);
-                        }
-                    }
+                    add_sums<kRW>(to, vref, o);
                     tc_fence_before_sync();
                 }
-                any_of<kSoft>(false);  // the maxima of all warps are there
+                any_of<kGroup>(false, g);  // the maxima of all warps are there
+                // each row's new reference, and what it makes of the sums so far
+                if (gt < R) {
+                    const float m = reinterpret_cast<const float *>(S.m[g])[gt];
+                    const float top = fmaxf(fmaxf(S.wmax[g][0][gt], S.wmax[g][1][gt]),
+                                            fmaxf(S.wmax[g][2][gt], S.wmax[g][3][gt]));
+                    float back = 1.0f;
+                    if (top > m) {
+                        back = ex2(m - (top + kHeadroom));
+                        reinterpret_cast<float *>(S.m[g])[gt] = reinterpret_cast<float *>(S.mref[g])[gt] = top + kHeadroom;
+                    }
+                    reinterpret_cast<float *>(S.back[g])[gt] = back;
+                }
+                any_of<kGroup>(false, g);
 #pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    const float top = fmaxf(fmaxf(S.wmax[wg][0][r], S.wmax[wg][1][r]),
-                                            fmaxf(S.wmax[wg][2][r], S.wmax[wg][3][r]));
-                    if (top > m[r]) {
-                        const float mn = top + kHeadroom, back = ex2(m[r] - mn);
-                        z[r] *= back;
-                        o[r] *= back;
-                        m[r] = mn;
+                for (int h = 0; h < kRW / 4; ++h) {
+                    const float4 back = S.back[g][r0 / 4 + h];
+                    const float bk[4] = {back.x, back.y, back.z, back.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        z[4 * h + e] *= bk[e];
+                        o[4 * h + e] *= bk[e];
                     }
                 }
                 if (vmax > 0.0f) {
@@ -454,102 +591,116 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                     inv_vref = 1.0f / vmax;
                 }
                 chain = 0;
-                any_of<kSoft>(false);  // the maxima have been read
             }
             // weights and their digits
-            uint32_t u[kRW];
-            {
-                const float up = f.vs[me >> 4] * inv_vref * 0x1p32f;
+            const float up = f.vs[me >> 4] * inv_vref * 0x1p32f;
+            wait(&S.p_empty[g], ((i >> 1) + 1) & 1, ok);  // PV of this group's last tile has read the buffer
+            if ((flags & kGroupFirst) && given > 0) wait(&S.sum_empty[g], (given - 1) & 1, ok);  // and the other group its sums
+            uint8_t *row = my_p + me * Sh::kNP;
 #pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    const float w = ex2(x[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
-                    z[r] += w;
-                    u[r] = to_u32_sat(w * up);
-                }
-            }
-            wait(&S.p_empty[i & 1], ((i >> 1) + 1) & 1, ok);  // PV of tile i - 2 has read this buffer
-            {
-                uint8_t *row = pbuf + (i & 1) * kPBytes + me * 128;
+            for (int h = 0; h < kRW / 4; ++h) {
+                const float4 m = S.mref[g][r0 / 4 + h];
+                const float w[4] = {ex2(x[4 * h] - m.x), ex2(x[4 * h + 1] - m.y), ex2(x[4 * h + 2] - m.z),
+                                    ex2(x[4 * h + 3] - m.w)};
 #pragma unroll
-                for (int h = 0; h < kRW / 4; ++h)
-                    *reinterpret_cast<uint4 *>(row + (((kRW / 4 * wg + h) ^ (me & 7)) << 4)) =
-                        make_uint4(u[4 * h], u[4 * h + 1], u[4 * h + 2], u[4 * h + 3]);
+                for (int e = 0; e < 4; ++e) z[4 * h + e] += w[e];
+                *reinterpret_cast<uint4 *>(row + (weights_chunk<R>(r0 / 4 + h, me) << 4)) =
+                    make_uint4(to_u32_sat(w[0] * up), to_u32_sat(w[1] * up), to_u32_sat(w[2] * up), to_u32_sat(w[3] * up));
             }
-            // (read before the weights are handed on: the stage and its info are free once PV has run)
-            Piece pc;
-            pc.valid = 1;
-            pc.ends = (flags & kEnds) != 0;
-            pc.b = f.b;
-            pc.head = f.head;
-            pc.rt = f.rt;
-            pc.units = f.units;
-            pc.u0 = u0 + i - f.k;
-            if (tid == 128) S.accumulate[i & 1] = chain > 0;
+            if (gt == 0) S.accumulate[g] = chain > 0;
             ++chain;
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.p_full[i & 1]);
+            if (lane == 0) mbar_arrive(&S.p_full[g]);
 
-            if (flags & kLast) {
-                // ---- the item, or this CTA's piece of it, is done
-                const Seq s = seq_of(pc.b);
-#pragma unroll
-                for (int r = 0; r < kRW; ++r) {
-                    const float y = warp_sum(z[r]);
-                    if (lane == 0) S.zsum[wg][w4][r] = y;
-                }
-                any_of<kSoft>(false);
-                wait(&S.p_empty[i & 1], (i >> 1) & 1, ok);
+            if (flags & kGroupLast) {
+                // ---- this group's part of the item is done
+                const float zw = sum_rows<kRW>(z, lane);
+                if (lane < kRW) S.zsum[g][w4][r0 + lane] = zw;
+                wait(&S.p_empty[g], (i >> 1) & 1, ok);
                 tc_fence_after_sync();
-                const bool complete = k_first == 0 && pc.ends;
-                const int slot = k_first > 0 ? 0 : 1;
-                float *rec = p.part + static_cast<int64_t>(2 * c + slot) * rec_floats(R);
+                add_sums<kRW>(to, vref, o);
+                tc_fence_before_sync();
+                chain = 0;
+                any_of<kGroup>(false, g);  // the sums of all warps are there
+                auto zrow = [&](int r) {
+                    return (S.zsum[g][0][r] + S.zsum[g][1][r]) + (S.zsum[g][2][r] + S.zsum[g][3][r]);
+                };
+                if (!(flags & kLast)) {
+                    // the other group has the item's last tile: hand this part over, in this group's weight buffer
+                    float *dst = reinterpret_cast<float *>(my_p) + me;
 #pragma unroll
-                for (int h = 0; h < kRW / 2; ++h) {
-                    uint32_t ov[8];
-                    tmem_ld8(tmem + lanes + Sh::kO + 4 * kRW * wg + 8 * h, ov);
-                    tmem_wait_ld();
+                    for (int r = 0; r < kRW; ++r) dst[(r0 + r) * kPD] = o[r];
+                    if (gt < R) S.sum_z[g][gt] = zrow(gt);
+                    if (gt < R / 4) S.sum_m[g][gt] = S.m[g][gt];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.sum_full[g]);
+                    ++given;
+                } else {
+                    const bool both = (flags & kBoth) != 0;
+                    const int og = g ^ 1;
+                    if (both) wait(&S.sum_full[og], taken & 1, ok);
+                    const Seq s = seq_of(f.b);
+                    const bool ends = (flags & kEnds) != 0, complete = k_first == 0 && ends;
+                    const int slot = k_first > 0 ? 0 : 1;
+                    float *rec = p.part + static_cast<int64_t>(2 * c + slot) * rec_floats(R);
+                    const float *src = reinterpret_cast<const float *>(pbuf + og * Sh::kPBytes) + me;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = 2 * h + e, rr = kRW * wg + r, row = R * pc.rt + rr;
-                        float t = static_cast<float>(static_cast<int>(ov[4 * e])) * 0x1p-32f;
-                        t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 1])), 0x1p-24f, t);
-                        t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 2])), 0x1p-16f, t);
-                        t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 3])), 0x1p-8f, t);
-                        t = fmaf(t, vref, o[r]);
-                        const float zz = (S.zsum[wg][0][r] + S.zsum[wg][1][r]) + (S.zsum[wg][2][r] + S.zsum[wg][3][r]);
-                        if (row < s.rows) {
+                    for (int q = 0; q < kRW; ++q) {
+                        const int r = r0 + q, rw = R * f.rt + r;
+                        if (rw < s.rows) {
+                            float m = reinterpret_cast<const float *>(S.m[g])[r], zz = zrow(r), t = o[q];
+                            if (both) {
+                                const float m1 = reinterpret_cast<const float *>(S.sum_m[og])[r], M = fmaxf(m, m1);
+                                const float ref = M == -INFINITY ? 0.0f : M, a0 = ex2(m - ref), a1 = ex2(m1 - ref);
+                                zz = zz * a0 + S.sum_z[og][r] * a1;
+                                t = t * a0 + src[r * kPD] * a1;
+                                m = M;
+                            }
                             if (complete) {
-                                const int ri = p.by_gq.quot(row);
-                                p.out[static_cast<int64_t>(s.start + ri) * p.ldo + (pc.head * p.GQ + row - ri * p.GQ) * kPD + me] =
+                                const int ri = p.by_gq.quot(rw);
+                                p.out[static_cast<int64_t>(s.start + ri) * p.ldo + (f.head * p.GQ + rw - ri * p.GQ) * kPD + me] =
                                     zz > 0.0f ? t / zz : 0.0f;
                             } else {
-                                rec[rr * kPD + me] = t;
-                                if (me == 0) *reinterpret_cast<float2 *>(rec + R * kPD + 2 * rr) = make_float2(m[r], zz);
+                                rec[r * kPD + me] = t;
+                                if (me == 0) *reinterpret_cast<float2 *>(rec + R * kPD + 2 * r) = make_float2(m, zz);
                             }
                         }
                     }
+                    if (both) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&S.sum_empty[og]);
+                        ++taken;
+                    }
+                    if (!complete && gt == 0) {
+                        Piece pc;
+                        pc.valid = 1;
+                        pc.ends = ends;
+                        pc.b = f.b;
+                        pc.head = f.head;
+                        pc.rt = f.rt;
+                        pc.units = f.units;
+                        pc.u0 = u0 + i - f.k;
+                        S.piece[slot] = pc;
+                    }
                 }
-                tc_fence_before_sync();
-                if (!complete && tid == 128) S.piece[slot] = pc;
-                chain = 0;
-                any_of<kSoft>(false);  // the sums have been read
+                any_of<kGroup>(false, g);  // the sums have been read
             }
         }
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 1) tmem_dealloc(tmem, Sh::kTmemCols);
+    if (warp == Sh::kWarpQK) tmem_dealloc(tmem, Sh::kTmemCols);
     const Piece pieces[2] = {S.piece[0], S.piece[1]};
     const bool cut[2] = {pieces[0].valid != 0, pieces[1].valid != 0};
-    merge_cut_items<R, kNT>(p, cut, pieces, ranges, 1, S.last, seq_of);
+    merge_cut_items<R, Sh::kThreads>(p, cut, pieces, ranges, 1, S.last, seq_of);
     pdl_launch_dependents();
 }
 
 template <int R>
-cudaError_t launch_rows(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int ctas, cudaStream_t s) {
+cudaError_t launch_rows(const AttnParams &p, const CacheMaps &maps, int ctas, cudaStream_t s) {
     static DeviceOnce once;
     int dev = 0;
     cudaError_t e = current_device(&dev);
@@ -559,17 +710,17 @@ cudaError_t launch_rows(const AttnParams &p, const CUtensorMap &km, const CUtens
                                     static_cast<int>(tc_smem<R>()));
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_tc_paged_kernel<R>, dim3(ctas), Shape<R>::kThreads, tc_smem<R>(), s, p, km, vm);
+    return launch_pdl(attn_tc_paged_kernel<R>, dim3(ctas), Shape<R>::kThreads, tc_smem<R>(), s, p, maps);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_tc(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int max_rows,
-                                int64_t span, int num_sms, cudaStream_t s) {
+cudaError_t launch_attention_tc(const AttnParams &p, const CacheMaps &maps, int max_rows, int64_t span, int num_sms,
+                                cudaStream_t s) {
     const int R = max_rows <= 8 ? 8 : 32;
     const int64_t tiles = std::min<int64_t>(p.v.B, p.v.T) * p.v.Hkv * ceil_div(max_rows, R) * ceil_div(span, kTok);
     const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({tiles, num_sms, kMaxCtas})));
-    return R == 8 ? launch_rows<8>(p, km, vm, ctas, s) : launch_rows<32>(p, km, vm, ctas, s);
+    return R == 8 ? launch_rows<8>(p, maps, ctas, s) : launch_rows<32>(p, maps, ctas, s);
 }
 
 }  // namespace tern
