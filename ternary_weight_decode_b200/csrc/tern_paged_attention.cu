@@ -78,6 +78,11 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = as_u32(__floats2half2_rn(x - f.x, y - f.y));
 }
 
+__device__ __noinline__ void wait_slow(uint64_t *bar, uint32_t parity) { mbar_wait_bounded(bar, parity); }
+__device__ __forceinline__ void wait_landed(uint64_t *bar, uint32_t parity) {
+    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity);
+}
+
 // Codes c0 c1 (low half of the pair's bytes) as fp16 x 2.  int8: 1024 + (c +
 // 128) has the code's bits as its low byte (fp16 spacing 1 there), and one
 // subtraction leaves c; the caller has flipped the sign bits.  e4m3: the
@@ -173,9 +178,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane l < kBatch keeps the cursor of tiles l, l + kBatch, ...: tile i of the range is in
         // info[i / kBatch % 2][i % kBatch]
         auto info = [&](int i) -> TileInfo & { return S.info[warp][(i / kBatch) & 1][i % kBatch]; };
-        if (lane < kBatch && lane < count) advance<kRows>(p, cur, lane, seq_of);
+        int step = lane;
         auto fill = [&](int i0) {
             if (lane < kBatch && i0 + lane < count) {
+                advance<kRows>(p, cur, step, seq_of);
+                step = kBatch;
                 TileInfo x;
                 x.j0 = cur.tl.block(cur.k) * kPB;
                 x.b = cur.b;
@@ -193,7 +200,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 info(i0 + lane) = x;
-                if (i0 + kBatch + lane < count) advance<kRows>(p, cur, kBatch, seq_of);
             }
             __syncwarp();
         };
@@ -209,9 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         };
-        fill(0);
-#pragma unroll
-        for (int i = 0; i < kStages; ++i) start(i);
 
         State st;
         uint32_t qhi[8][2], qlo[8][2];
@@ -220,7 +223,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pos = 0, p_min = 0, p_max = 0, k_first = 0;
         uint32_t phases = 0;  // parity of each stage
         int stage = 0;
-        for (int i = 0; i < count; ++i) {
+#pragma unroll 1
+        for (int i = -1; i < count; ++i) {
+            // look up the first batch, and the batch behind the next while this one is worked off
+            if (i < 0 || (i % kBatch == 0 && i + kBatch < count)) fill(i < 0 ? 0 : i + kBatch);
+            if (i < 0) {
+#pragma unroll 1
+                for (int e = 0; e < kStages; ++e) start(e);
+                continue;
+            }
             const TileInfo x = info(i);
             if (i == 0 || (x.k >> 1) == 0) {
                 // ---- a new item: row g's query, dimensions 32 t .. 32 t + 31, as hi + lo operands
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int n = 0; n < 16; ++n) st.o[n] = make_float2(0.0f, 0.0f);
             }
             if (x.bi >= 0) {
-                mbar_wait_bounded(&S.bars[warp][stage], (phases >> stage) & 1u);
+                wait_landed(&S.bars[warp][stage], (phases >> stage) & 1u);
                 phases ^= 1u << stage;
                 const uint8_t *kt = my_ring + stage * kStageBytes, *vt = kt + kTileBytes;
                 // scores: tokens j0 + 2t, + 1 (n = 0) and j0 + 8 + 2t, + 1 (n = 1) of row g
@@ -345,8 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();  // these reads before the refill of the stage
                 __syncwarp();
             }
-            // the tiles behind the next batch's, while this one's are worked off (at tile 0 behind its queries)
-            if (i % kBatch == 0 && i + kBatch < count) fill(i + kBatch);
             start(i + kStages);
             stage = stage + 1 == kStages ? 0 : stage + 1;
 
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         Piece pc;
                         pc.valid = 1;
                         pc.ends = ends;
-                        pc.b = x.b;
+                        pc.s = s;
                         pc.head = x.head;
                         pc.rt = x.rt;
                         pc.u0 = u0 + i - (x.k >> 1);
@@ -408,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned first_ends = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].ends);
     const unsigned last_ok = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][1].valid);
     // bit 0: the first piece of warp 0, bit a + 1: the last piece of warp a
+#pragma unroll 1
     for (unsigned groups = (first_ok & 1u) | last_ok << 1; groups != 0; groups &= groups - 1) {
         const int a = __ffs(groups) - 2, w0 = max(a, 0), slot0 = a < 0 ? 0 : 1;
         const Piece pc = S.piece[w0][slot0];
@@ -424,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (slot0 == 0) cut[0] = true; else cut[1] = true;
             if (slot0 == 0) shared_piece[0] = pc; else shared_piece[1] = pc;
         }
-        const Seq s = seq_of(pc.b);
+        const Seq s = pc.s;
         for (int rr = warp; rr < kRows; rr += kWarps) {
             const int row = kRows * pc.rt + rr;
             if (row >= s.rows) break;
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    merge_cut_items<kRows, kThreads>(p, cut, shared_piece, R, kWarps, S.last, seq_of);
+    merge_cut_items<kRows, kThreads>(p, cut, shared_piece, R, kWarps, S.last);
     pdl_launch_dependents();
 }
 

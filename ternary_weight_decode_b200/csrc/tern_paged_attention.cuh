@@ -88,8 +88,16 @@ __device__ __forceinline__ int tile_count(const Tiles &t) {
 template <int R, int TB>
 __device__ __forceinline__ long long head_units(const AttnParams &p, const Seq &s) {
     long long u = 0;
+#pragma unroll 1
     for (int rt = 0; rt * R < s.rows; ++rt) u += tile_count<TB>(tiles_of<R>(p, s, rt));
     return u;
+}
+
+// 1 / x within a rounding error (x not subnormal), 0 for x = 0.
+__device__ __forceinline__ float recip(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return x > 0.0f ? y : 0.0f;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -129,6 +137,7 @@ struct Cursor {
 template <int R, int TB, typename SeqOf>
 __device__ __forceinline__ void advance(const AttnParams &p, Cursor<TB> &x, int n, SeqOf seq_of) {
     x.k += n;
+#pragma unroll 1
     while (x.k >= x.units()) {
         x.k -= x.units();
         ++x.ord;
@@ -138,6 +147,7 @@ __device__ __forceinline__ void advance(const AttnParams &p, Cursor<TB> &x, int 
             x.rt = 0;
             if (++x.head == p.v.Hkv) {
                 x.head = 0;
+#pragma unroll 1
                 do {
                     if (++x.b >= p.v.B) return;  // past the line: the caller counts its tiles
                     x.s = seq_of(x.b);
@@ -167,6 +177,7 @@ __device__ __forceinline__ Line make_line(const AttnParams &p, LineShared<NT> &S
     Line L;
     L.per = (v.B + NT - 1) / NT;
     long long mine = 0;
+#pragma unroll 1
     for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b) {
         const Seq s = sequence(p, b);
         mine += v.Hkv * head_units<R, TB>(p, s);
@@ -199,13 +210,14 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
     const int lane = threadIdx.x & 31;
     Cursor<TB> cur;
     int lo = 0;  // the last thread whose sequences begin at or before u
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < NT / 32 && 32 * i * L.per < p.v.B; ++i) {
         const unsigned le = __ballot_sync(0xffffffffu, S.chunk[32 * i + lane] <= u);
         if (le) lo = 32 * i + 31 - __clz(le);
     }
     long long off = u - S.chunk[lo], ph;
     int b = lo * L.per;
+#pragma unroll 1
     for (;; ++b) {
         cur.s = seq_of(b);
         ph = head_units<R, TB>(p, cur.s);
@@ -217,6 +229,7 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
     off -= cur.head * ph;
     cur.rt = 0;
     cur.tl = tiles_of<R>(p, cur.s, 0);
+#pragma unroll 1
     while (off >= cur.units()) {
         off -= cur.units();
         cur.tl = tiles_of<R>(p, cur.s, ++cur.rt);
@@ -228,7 +241,7 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
 
 // Row rr of an item to its place in out: four dimensions a lane.
 __device__ __forceinline__ void write_row(const AttnParams &p, int start, int head, int row, float4 o, float z, int d) {
-    const float iz = z > 0.0f ? 1.0f / z : 0.0f;
+    const float iz = recip(z);
     const int i = p.by_gq.quot(row);
     *reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(start + i) * p.ldo +
                                 (head * p.GQ + row - i * p.GQ) * kPD + d) =
@@ -246,24 +259,27 @@ __device__ __forceinline__ void add_scaled(float4 &o, float &z, float f, float4 
 // A piece of a cut item.
 struct Piece {
     int valid, ends;   // ends: holds the item's last tile
-    int b, head, rt, units;
+    int head, rt, units;
+    Seq s;
     long long u0;      // line index of the item's first tile
 };
+
+constexpr int kMergeParts = 10;
 
 // Items cut between CTAs: cut[0]: the CTA's range begins inside pc[0], whose
 // record lies in slot 2c; cut[1]: it ends inside pc[1] (slot 2c + 1; the
 // middle CTAs of an item have slot 2c alone).  Whoever finishes an item's last
 // part merges all of them in range order.  All threads of the CTA, after
 // their writes of the records; per_cta: ranges of the line in one CTA.
-template <int R, int NT, typename SeqOf>
+template <int R, int NT>
 __device__ __forceinline__ void merge_cut_items(const AttnParams &p, const bool (&cut)[2], const Piece (&pc)[2],
-                                                const Ranges &ranges, int per_cta, int (&last)[2], SeqOf seq_of) {
+                                                const Ranges &ranges, int per_cta, int (&last)[2]) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (!cut[0] && !cut[1]) return;
     __threadfence();
     __syncthreads();
     int first[2], parts[2];
-#pragma unroll
+#pragma unroll 1
     for (int a = 0; a < 2; ++a) {
         first[a] = parts[a] = 0;
         if (!cut[a]) continue;
@@ -276,37 +292,45 @@ __device__ __forceinline__ void merge_cut_items(const AttnParams &p, const bool 
         }
     }
     __syncthreads();
-#pragma unroll
+#pragma unroll 1
     for (int a = 0; a < 2; ++a) {
         if (!cut[a] || !last[a]) continue;
         __threadfence();
-        const Seq s = seq_of(pc[a].b);
+        const Seq s = pc[a].s;
+        // part i's record: slot 2 first + 1 for the first, 2 (first + i) behind it
+        const float *base = p.part + static_cast<int64_t>(2 * first[a]) * rec_floats(R);
+        auto offset = [](int i) { return (i == 0 ? 1 : 2 * i) * rec_floats(R); };
+#pragma unroll 1
         for (int rr = warp; rr < R; rr += NT / 32) {
             const int row = R * pc[a].rt + rr;
             if (row >= s.rows) break;
-            auto record = [&](int i) {
-                return p.part + static_cast<int64_t>(2 * (first[a] + i) + (i == 0 ? 1 : 0)) * rec_floats(R);
-            };
+            const float *sums = base + rr * kPD + 4 * lane, *stats = base + R * kPD + 2 * rr;
             float z = 0.0f, M = -INFINITY;
             float4 o = make_float4(0, 0, 0, 0);
-            for (int i0 = 0; i0 < parts[a]; i0 += 16) {  // 16 parts at a time: their loads are all in flight at once
-                const int n = min(16, parts[a] - i0);
+#pragma unroll 1
+            for (int i0 = 0; i0 < parts[a]; i0 += kMergeParts) {  // so many at a time: their loads are all in flight at once
+                const int n = min(kMergeParts, parts[a] - i0);
                 float2 mz = make_float2(-INFINITY, 0.0f);
-                if (lane < n) mz = __ldcg(reinterpret_cast<const float2 *>(record(i0 + lane) + R * kPD + 2 * rr));
-                float4 x[16];
+                if (lane < n) mz = __ldcg(reinterpret_cast<const float2 *>(stats + offset(i0 + lane)));
+                float4 x[kMergeParts];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < n) x[i] = __ldcg(reinterpret_cast<const float4 *>(record(i0 + i) + rr * kPD + 4 * lane));
+                for (int i = 0; i < kMergeParts; ++i)
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(sums + offset(i0 + min(i, n - 1))));
                 const float Mn = fmaxf(M, warp_max(mz.x));
                 const float ref = Mn == -INFINITY ? 0.0f : Mn;
                 const float back = ex2(M - ref);
-                z *= back;
-                o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
                 M = Mn;
-                const float f = ex2(mz.x - ref);
+                const float f = ex2(mz.x - ref);  // 0 past the last part
+                z = z * back + warp_sum(f * mz.y);
+                o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < n) add_scaled(o, z, __shfl_sync(0xffffffffu, f, i), x[i], __shfl_sync(0xffffffffu, mz.y, i));
+                for (int i = 0; i < kMergeParts; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i);
+                    o.x = fmaf(fi, x[i].x, o.x);
+                    o.y = fmaf(fi, x[i].y, o.y);
+                    o.z = fmaf(fi, x[i].z, o.z);
+                    o.w = fmaf(fi, x[i].w, o.w);
+                }
             }
             write_row(p, s.start, pc[a].head, row, o, z, 4 * lane);
         }

@@ -49,7 +49,7 @@ constexpr int kTB = 8;                    // blocks of a tile
 constexpr int kTok = kTB * kPB;           // 128 tokens
 constexpr int kTileBytes = kTok * kPD;    // 16 KB of K or V codes
 constexpr int kInfo = 16;                 // tile infos kept: K's ring runs at most kStages + kSBufs + 2 tiles ahead of the softmax
-constexpr int kRowf = 8;                  // items whose score scales are kept (the digits run four ahead at most)
+constexpr int kItems = 8;                 // items kept for the query warp, and whose score scales are kept
 constexpr float kHeadroom = 6.0f;         // a new reference lies this far (log2) above the largest score
 constexpr int kMaxChain = 256;            // tiles summed in int32: 256 * 128 * 255 * 127 < 2^31
 constexpr float kVRange = 1.0f / 256.0f;  // largest block scale of a tile, relative to the reference
@@ -79,10 +79,19 @@ struct Shape {
 struct TileInfo {
     float ks[kTB], vs[kTB];
     int j0[kTB];      // first token of each block
+    int row[kTB];     // its first code row, for the block that begins a copy
+    int size[kTB];    // log2 of the blocks that this copy takes, -1: none begins here
     int valid;        // bit j: block j is there
     int flags;
     float vmax;       // largest value scale
-    int b, head, rt, k, units, ord;
+    int head, rt, k, units, ord;
+    Seq s;
+};
+// An item, as the query warp sees it.
+struct ItemInfo {
+    int head, rt;
+    int tiles;        // of this CTA
+    Seq s;
 };
 enum : int {
     kFirst = 1,       // the first tile of its item in this CTA
@@ -98,15 +107,17 @@ template <int R>
 struct TcShared {
     using Sh = Shape<R>;
     TileInfo info[kInfo];
-    float4 rowf[kRowf][R / 4];        // score scale of each row's digits
+    ItemInfo item[kItems];
+    float4 rowf[kItems][R / 4];        // score scale of each row's digits
     float4 m[2][R / 4], mref[2][R / 4];  // each group's references; mref: 0 for a row that has seen nothing
     float4 back[2][R / 4];            // what new references make of the sums before
     float wmax[2][4][R];
     float zsum[2][4][R];
-    float4 sum_m[2][R / 4];           // a group's references and sums when it hands its part of an item over
-    float sum_z[2][R];
+    float sum_m[2][R], sum_z[2][R];   // a group's references and sums when it hands its part of an item over
+    float2 factors[2][R];             // of the parts at an item's end
     LineShared<Sh::kThreads> line;
     uint64_t k_full[Sh::kStages], k_empty[Sh::kStages], v_full[Sh::kStages], v_empty[Sh::kStages];
+    uint64_t info_full[kInfo], item_full[kItems], item_empty[kItems];
     uint64_t s_full[Sh::kSBufs], s_empty[Sh::kSBufs], p_full[2], p_empty[2], q_full[2], q_empty[2], sum_full[2], sum_empty[2];
     Piece piece[2];
     uint32_t tmem;
@@ -137,8 +148,9 @@ __device__ __forceinline__ int weights_chunk(int c, int k) {
 }
 
 // A wait of this thread; once one has run out, none of the later ones waits.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
-    if (ok) ok = mbar_wait_bounded(bar, parity);
+    if (ok && !mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity);
 }
 
 // An int32 of at most 22 bits as fp32, exactly, without the conversion unit.
@@ -210,48 +222,55 @@ __device__ __forceinline__ void add_sums(uint32_t taddr, float vref, float (&o)[
     }
 }
 
-// The copies of K's or V's blocks, or of both, of a range's tiles; K's also
-// writes the tiles' infos.
-template <int R, bool IS_K, bool IS_V, typename SeqOf>
-__device__ __forceinline__ void copy_blocks(const AttnParams &p, const CacheMaps &maps, TcShared<R> &S, uint8_t *kring,
-                                            uint8_t *vring, const Line &L, long long u0, int count, SeqOf seq_of) {
+// Look-up of a range's tiles, and K's copies (with COPY_V, V's too): writes the
+// infos of the items and tiles.
+template <int R, bool COPY_V, typename SeqOf>
+__device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &maps, TcShared<R> &S, uint8_t *kring,
+                                          uint8_t *vring, const Line &L, long long u0, int count, SeqOf seq_of) {
     constexpr int kSt = Shape<R>::kStages;
     const PagedView &v = p.v;
     const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
     bool ok = true;
-    // blocks of the tiles, four tiles at a time (lane = 8 * tile + block)
-    Cursor<kTB> cur = find_place<R, kTB>(p, S.line, L, u0, seq_of), at = cur;
-    if (sub < count) advance<R>(p, cur, sub, seq_of);
-    int bi = -1, j0 = 0;
+    // four tiles at a time (lane = 8 * tile + block): a batch is looked up while the one before is copied
+    Cursor<kTB> cur = find_place<R, kTB>(p, S.line, L, u0, seq_of);
+    int step = sub, bi = -1, j0 = 0;
     float ks = 0.0f, vs = 0.0f;
-    auto look_up = [&](int i0) {  // this lane's block of tile i0 + sub
+#pragma unroll 1
+    for (int i0 = 0; i0 < count + 4; i0 += 4) {
+        const int b_now = bi, j0_now = j0;
+        const float ks_now = ks, vs_now = vs;
+        const Cursor<kTB> it = cur;
         bi = -1;
         ks = vs = 0.0f;
-        if (i0 + sub >= count) return;
-        at = cur;
-        const int kb = kTB * cur.k + j;
-        if (kb < cur.tl.n) {
-            const int blk = cur.tl.block(kb);
-            j0 = blk * kPB;
-            const int64_t x = block_index(v, cur.b, blk);
-            if (x >= 0) {
-                bi = static_cast<int>(x) + cur.head * v.bpp;
-                if (IS_K) {
+        if (i0 + sub < count) {  // this lane's block of tile i0 + sub
+            advance<R>(p, cur, step, seq_of);
+            step = 4;
+            if (j == 0 && (cur.k == 0 || i0 + sub == 0)) {
+                const int slot = cur.ord % kItems;
+                wait(&S.item_empty[slot], ((cur.ord / kItems) + 1) & 1, ok);
+                S.item[slot].head = cur.head;
+                S.item[slot].rt = cur.rt;
+                S.item[slot].tiles = min(cur.units() - cur.k, count - i0 - sub);
+                S.item[slot].s = cur.s;
+                mbar_arrive(&S.item_full[slot]);
+            }
+            const int kb = kTB * cur.k + j;
+            if (kb < cur.tl.n) {
+                const int blk = cur.tl.block(kb);
+                j0 = blk * kPB;
+                const int64_t x = block_index(v, cur.b, blk);
+                if (x >= 0) {
+                    bi = static_cast<int>(x) + cur.head * v.bpp;
                     ks = v.ks[bi];
                     vs = v.vs[bi];
                 }
             }
         }
-        if (i0 + 4 + sub < count) advance<R>(p, cur, 4, seq_of);
-    };
-    look_up(0);
-    for (int i0 = 0; i0 < count; i0 += 4) {
-        const int b_now = bi, j0_now = j0;
-        const float ks_now = ks, vs_now = vs;
-        const Cursor<kTB> it = at;
+        __syncwarp();
+        if (i0 == 0) continue;
         const unsigned there = __ballot_sync(0xffffffffu, b_now >= 0);
         // runs of blocks that lie behind one another in the cache: one copy each for 8, 4, 2 or 1 of them
-        // (a copy of 16 rows takes as long as one of 64: 2150 cycles a tile in single blocks, 1690 in 64 rows)
+        // (copies of 16 rows: 2150 cycles a tile, of 64 rows 1690)
         const int before = __shfl_up_sync(0xffffffffu, b_now, 1);
         const unsigned follows = __ballot_sync(0xffffffffu, b_now >= 0 && b_now == before + 1) >> (8 * sub);
         int size = 0;  // log2 of the blocks this lane copies, -1: another lane does
@@ -259,28 +278,26 @@ __device__ __forceinline__ void copy_blocks(const AttnParams &p, const CacheMaps
         else if ((follows >> (j & 4) & 0xEu) == 0xEu) size = 2;
         else if (follows >> (j & 6) & 2u) size = 1;
         if (b_now < 0 || (j & ((1 << size) - 1))) size = -1;
-        unsigned not_whole = 0;
-        float vmax = 0.0f;
-        if (IS_K) {
-            // masks: a block whose tokens not every row sees, or that is missing
-            const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
-            const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
-            const bool whole = b_now >= 0 && j0_now + kPB - 1 <= p_min &&
-                               (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
-            not_whole = __ballot_sync(0xffffffffu, !whole);
-            vmax = vs_now;
+        // masks: a block whose tokens not every row sees, or that is missing
+        const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
+        const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
+        const bool whole = b_now >= 0 && j0_now + kPB - 1 <= p_min &&
+                           (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
+        const unsigned not_whole = __ballot_sync(0xffffffffu, !whole);
+        float vmax = vs_now;
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-        }
-        if (i0 + 4 < count) look_up(i0 + 4);  // in flight while the stages come free
-        for (int e = 0; e < 4 && i0 + e < count; ++e) {
-            const int i = i0 + e, stage = i % kSt;
-            if (IS_K) wait(&S.k_empty[stage], ((i / kSt) + 1) & 1, ok);
-            if (IS_K && sub == e) {
+        for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+#pragma unroll 1
+        for (int e = 0; e < 4 && i0 - 4 + e < count; ++e) {
+            const int i = i0 - 4 + e, stage = i % kSt;
+            wait(&S.k_empty[stage], ((i / kSt) + 1) & 1, ok);
+            if (sub == e) {
                 TileInfo &f = S.info[i % kInfo];
                 f.ks[j] = ks_now;
                 f.vs[j] = vs_now;
                 f.j0[j] = j0_now;
+                f.row[j] = b_now * kPB;
+                f.size[j] = size;
                 if (j == 0) {
                     const int since = min(it.k, i), left = min(it.units() - 1 - it.k, count - 1 - i);
                     f.valid = there >> (8 * e) & 255;
@@ -288,36 +305,62 @@ __device__ __forceinline__ void copy_blocks(const AttnParams &p, const CacheMaps
                               (left < 2 ? kGroupLast : 0) | (since + left > 0 ? kBoth : 0) |
                               ((not_whole >> (8 * e) & 255) ? kEdge : 0) | (it.k + 1 == it.units() ? kEnds : 0);
                     f.vmax = vmax;
-                    f.b = it.b;
                     f.head = it.head;
                     f.rt = it.rt;
                     f.k = it.k;
                     f.units = it.units();
                     f.ord = it.ord;
+                    f.s = it.s;
                 }
             }
             const uint32_t bytes = __popc(there >> (8 * e) & 255) * kPB * kPD;
-            const int at_stage = stage * kTileBytes + j * kPB * kPD;
-            if (IS_K) {
-                __syncwarp();
-                if (lane == 8 * e) mbar_arrive_expect_tx(&S.k_full[stage], bytes);
-                __syncwarp();
-                if (sub == e && size >= 0) tma_load_2d_nohint(kring + at_stage, &maps.k[size], 0, b_now * kPB, &S.k_full[stage]);
+            const int at = stage * kTileBytes + j * kPB * kPD;
+            __syncwarp();
+            if (lane == 8 * e) {
+                mbar_arrive_expect_tx(&S.k_full[stage], bytes);
+                mbar_arrive(&S.info_full[i % kInfo]);
             }
-            if (IS_V) {
+            __syncwarp();
+            if (sub == e && size >= 0) tma_load_2d_nohint(kring + at, &maps.k[size], 0, b_now * kPB, &S.k_full[stage]);
+            if (COPY_V) {
                 wait(&S.v_empty[stage], ((i / kSt) + 1) & 1, ok);
                 if (lane == 8 * e) mbar_arrive_expect_tx(&S.v_full[stage], bytes);
                 __syncwarp();
-                if (sub == e && size >= 0) tma_load_2d_nohint(vring + at_stage, &maps.v[size], 0, b_now * kPB, &S.v_full[stage]);
+                if (sub == e && size >= 0)
+                    tma_load_2d_nohint(vring + at, &maps.v[size], 0, b_now * kPB, &S.v_full[stage]);
             }
         }
     }
     // no copy is in flight when the CTA ends, even after a wait that ran out
     bool land = true;
+#pragma unroll 1
     for (int i = max(0, count - kSt); i < count; ++i) {
-        if (IS_K) wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
-        if (IS_V) wait(&S.v_full[i % kSt], (i / kSt) & 1, land);
+        wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
+        if (COPY_V) wait(&S.v_full[i % kSt], (i / kSt) & 1, land);
     }
+}
+
+// V's copies, by the tiles' infos; lanes 0-7 a block each.
+template <int R>
+__device__ __forceinline__ void copy_values(const CacheMaps &maps, TcShared<R> &S, uint8_t *vring, int count) {
+    constexpr int kSt = Shape<R>::kStages;
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        const int stage = i % kSt;
+        wait(&S.info_full[i % kInfo], (i / kInfo) & 1, ok);
+        const TileInfo &f = S.info[i % kInfo];
+        const int size = lane < kTB ? f.size[lane] : -1, row = lane < kTB ? f.row[lane] : 0;
+        wait(&S.v_empty[stage], ((i / kSt) + 1) & 1, ok);
+        if (lane == 0) mbar_arrive_expect_tx(&S.v_full[stage], __popc(f.valid) * kPB * kPD);
+        __syncwarp();
+        if (size >= 0)
+            tma_load_2d_nohint(vring + stage * kTileBytes + lane * kPB * kPD, &maps.v[size], 0, row, &S.v_full[stage]);
+    }
+    bool land = true;
+#pragma unroll 1
+    for (int i = max(0, count - kSt); i < count; ++i) wait(&S.v_full[i % kSt], (i / kSt) & 1, land);
 }
 
 template <int R>
@@ -355,6 +398,11 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             mbar_init(&S.sum_empty[i], 4 * Sh::kHalves);
             S.piece[i].valid = 0;
         }
+        for (int i = 0; i < kInfo; ++i) mbar_init(&S.info_full[i], 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&S.item_full[i], 1);
+            mbar_init(&S.item_empty[i], 1);
+        }
         for (int i = 0; i < Sh::kSBufs; ++i) {
             mbar_init(&S.s_full[i], 2);
             mbar_init(&S.s_empty[i], 4 * Sh::kHalves);
@@ -369,7 +417,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
     tc_fence_before_sync();
     const Line L = make_line<R, kTB>(p, S.line);  // (holds two __syncthreads)
     tc_fence_after_sync();
-    auto seq_of = [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); };
     const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), L.total));
     Ranges ranges = {0, 0};
     if (L.total > 0) {
@@ -382,14 +429,16 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
 
     if (count == 0) {
     } else if (warp == Sh::kWarpK) {
-        copy_blocks<R, true, Sh::kWarpV < 0>(p, maps, S, kring, vring, L, u0, count, seq_of);
+        auto seq_of = [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); };
+        copy_keys<R, (Sh::kWarpV < 0)>(p, maps, S, kring, vring, L, u0, count, seq_of);
     } else if (warp == Sh::kWarpV) {
-        copy_blocks<R, false, true>(p, maps, S, kring, vring, L, u0, count, seq_of);
+        copy_values<R>(maps, S, vring, count);
     } else if (warp == Sh::kWarpQK) {
         // ---- S of each tile, as soon as its keys are there and its accumulator has been read
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_i8(128, Sh::kNS, 1, 1);
             int item = -1;
+#pragma unroll 1
             for (int i = 0; i < count; ++i) {
                 const int stage = i % kSt, buf = i % Sh::kSBufs;
                 wait(&S.k_full[stage], (i / kSt) & 1, ok);
@@ -415,6 +464,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
         // ---- O of each tile, added to its group's sums
         if (lane == 0) {
             constexpr uint32_t id_o = idesc_i8(128, Sh::kNP, 1, 0) | (1u << 15) | (1u << 16);  // both operands M/N-major
+#pragma unroll 1
             for (int i = 0; i < count; ++i) {
                 const int stage = i % kSt, g = i & 1;
                 wait(&S.v_full[stage], (i / kSt) & 1, ok);
@@ -433,47 +483,65 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
         __syncwarp();
     } else if (warp == Sh::kWarpQ) {
         // ---- query digits of each item, ahead of its tiles
-        Cursor<kTB> cur = find_place<R, kTB>(p, S.line, L, u0, seq_of);
+#pragma unroll 1
         for (int done = 0, item = 0; done < count; ++item) {
+            const int slot = item % kItems;
+            wait(&S.item_full[slot], (item / kItems) & 1, ok);
+            const ItemInfo it = S.item[slot];
             wait(&S.q_empty[item & 1], ((item >> 1) + 1) & 1, ok);
             uint8_t *qb = qbuf + (item & 1) * Sh::kQBytes;
-#pragma unroll 8
-            for (int rr = 0; rr < R; ++rr) {
-                const int row = R * cur.rt + rr;
-                float4 x = make_float4(0, 0, 0, 0);
-                if (row < cur.s.rows) {
-                    const int ri = p.by_gq.quot(row);
-                    x = *reinterpret_cast<const float4 *>(p.q + static_cast<int64_t>(cur.s.start + ri) * p.ldq +
-                                                          (cur.head * p.GQ + row - ri * p.GQ) * kPD + 4 * lane);
+#pragma unroll 1
+            for (int rr0 = 0; rr0 < R; rr0 += 4) {
+                float4 x[4];
+                float up[4], down[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int row = R * it.rt + rr0 + h;
+                    x[h] = make_float4(0, 0, 0, 0);
+                    if (row < it.s.rows) {
+                        const int ri = p.by_gq.quot(row);
+                        x[h] = *reinterpret_cast<const float4 *>(p.q + static_cast<int64_t>(it.s.start + ri) * p.ldq +
+                                                                 (it.head * p.GQ + row - ri * p.GQ) * kPD + 4 * lane);
+                    }
                 }
-                const float amax = warp_max(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-                // the row times 2^e: its largest value in [2^21, 2^22), so that three signed digits hold it
-                const int e = max(-120, min(120, 148 - static_cast<int>(__float_as_uint(amax) >> 23)));
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                const int n[4] = {__float2int_rn(x.x * up), __float2int_rn(x.y * up), __float2int_rn(x.z * up),
-                                  __float2int_rn(x.w * up)};
-                // digits: (n + 0x8080) ^ 0x8080 has the signed digits d0, d1 as its low bytes, d2 above
-                uint32_t w[3] = {0, 0, 0};
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const uint32_t t = static_cast<uint32_t>(n[d] + 0x8080) ^ 0x8080u;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) w[k] |= (t >> (8 * k) & 255u) << (8 * d);
+                for (int h = 0; h < 4; ++h) {
+                    const float amax = redux_max(fmaxf(fmaxf(fabsf(x[h].x), fabsf(x[h].y)), fmaxf(fabsf(x[h].z), fabsf(x[h].w))));
+                    // the row times 2^e: its largest value in [2^21, 2^22), so that three signed digits hold it
+                    const int e = max(-120, min(120, 148 - static_cast<int>(__float_as_uint(amax) >> 23)));
+                    up[h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    down[h] = R * it.rt + rr0 + h < it.s.rows
+                                  ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                                  : 0.0f;
                 }
-                // column of digit k of row rr: 6 (rr / 2) + 2 k + rr % 2, so that two rows' digits are neighbours
+                if (lane == 0) S.rowf[slot][rr0 / 4] = make_float4(down[0], down[1], down[2], down[3]);
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint32_t *>(qb + sw128_offset(6 * (rr >> 1) + 2 * k + (rr & 1), 4 * lane)) = w[k];
-                if (lane == 0)
-                    reinterpret_cast<float *>(S.rowf[item % kRowf])[rr] =
-                        row < cur.s.rows ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.0f;
+                for (int h = 0; h < 4; ++h) {
+                    const int rr = rr0 + h;
+                    // digits: (n + 0x8080) ^ 0x8080 has the signed digits d0, d1 as its low bytes, d2 above
+                    const float f[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
+                    uint32_t n[4];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        n[d] = static_cast<uint32_t>(__float2int_rn(f[d] * up[h]) + 0x8080) ^ 0x8080u;
+                    // digit k of the four dimensions as one word; column of digit k of row rr: 6 (rr / 2) + 2 k + rr % 2,
+                    // so that two rows' digits are neighbours
+                    const uint32_t lo0 = __byte_perm(n[0], n[1], 0x5140), lo1 = __byte_perm(n[2], n[3], 0x5140);
+                    const uint32_t hi0 = __byte_perm(n[0], n[1], 0x0062), hi1 = __byte_perm(n[2], n[3], 0x0062);
+                    const uint32_t w[3] = {__byte_perm(lo0, lo1, 0x5410), __byte_perm(lo0, lo1, 0x7632),
+                                           __byte_perm(hi0, hi1, 0x5410)};
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        *reinterpret_cast<uint32_t *>(qb + sw128_offset(6 * (rr >> 1) + 2 * k + (rr & 1), 4 * lane)) = w[k];
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.q_full[item & 1]);
-            const int n = min(count - done, cur.units() - cur.k);
-            done += n;
-            if (done < count) advance<R>(p, cur, n, seq_of);
+            if (lane == 0) {
+                mbar_arrive(&S.q_full[item & 1]);
+                mbar_arrive(&S.item_empty[slot]);
+            }
+            done += it.tiles;
         }
     } else if (warp >= Sh::kHelpers) {
         // ---- softmax group g: tiles g, g + 2, ...; thread = token of the tile and dimension of the output, rows
@@ -487,6 +555,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
         float vref = 1.0f, inv_vref = 1.0f;
         int chain = 0, k_first = 0;
         int given = 0, taken = 0;  // items handed to the other group, and taken from it
+#pragma unroll 1
         for (int i = g; i < count; i += 2) {
             const TileInfo &f = S.info[i % kInfo];
             const int buf = i % Sh::kSBufs;
@@ -514,7 +583,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 3; ++e) tmem_ld8(ts + buf * Sh::kNS + 24 * h + 8 * e, *reinterpret_cast<uint32_t(*)[8]>(sv + 8 * e));
                     tmem_wait_ld();
-                    const float4 ra = S.rowf[f.ord % kRowf][r0 / 4 + 2 * h], rb = S.rowf[f.ord % kRowf][r0 / 4 + 2 * h + 1];
+                    const float4 ra = S.rowf[f.ord % kItems][r0 / 4 + 2 * h], rb = S.rowf[f.ord % kItems][r0 / 4 + 2 * h + 1];
                     const float2 rf[4] = {make_float2(ra.x, ra.y), make_float2(ra.z, ra.w), make_float2(rb.x, rb.y),
                                           make_float2(rb.z, rb.w)};
 #pragma unroll
@@ -533,7 +602,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&S.s_empty[buf]);
             }
             if (flags & kEdge) {
-                const Seq s = seq_of(f.b);
+                const Seq s = f.s;
                 const int tok = f.j0[me >> 4] + (me & 15);
                 const bool there = f.valid >> (me >> 4) & 1;
 #pragma unroll
@@ -588,7 +657,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                 }
                 if (vmax > 0.0f) {
                     vref = vmax;
-                    inv_vref = 1.0f / vmax;
+                    inv_vref = recip(vmax);
                 }
                 chain = 0;
             }
@@ -623,50 +692,54 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                 add_sums<kRW>(to, vref, o);
                 tc_fence_before_sync();
                 chain = 0;
-                any_of<kGroup>(false, g);  // the sums of all warps are there
-                auto zrow = [&](int r) {
-                    return (S.zsum[g][0][r] + S.zsum[g][1][r]) + (S.zsum[g][2][r] + S.zsum[g][3][r]);
-                };
-                if (!(flags & kLast)) {
-                    // the other group has the item's last tile: hand this part over, in this group's weight buffer
-                    float *dst = reinterpret_cast<float *>(my_p) + me;
+                // the sums, by dimension, where the weights lay
+                float *own = reinterpret_cast<float *>(my_p) + me;
 #pragma unroll
-                    for (int r = 0; r < kRW; ++r) dst[(r0 + r) * kPD] = o[r];
-                    if (gt < R) S.sum_z[g][gt] = zrow(gt);
-                    if (gt < R / 4) S.sum_m[g][gt] = S.m[g][gt];
+                for (int r = 0; r < kRW; ++r) own[(r0 + r) * kPD] = o[r];
+                any_of<kGroup>(false, g);
+                const float zr = gt < R ? (S.zsum[g][0][gt] + S.zsum[g][1][gt]) + (S.zsum[g][2][gt] + S.zsum[g][3][gt]) : 0.0f;
+                if (!(flags & kLast)) {
+                    // the other group has the item's last tile: hand this part over
+                    if (gt < R) {
+                        S.sum_z[g][gt] = zr;
+                        S.sum_m[g][gt] = reinterpret_cast<const float *>(S.m[g])[gt];
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.sum_full[g]);
                     ++given;
                 } else {
-                    const bool both = (flags & kBoth) != 0;
-                    const int og = g ^ 1;
+                    const bool both = (flags & kBoth) != 0, ends = (flags & kEnds) != 0, complete = k_first == 0 && ends;
+                    const int og = g ^ 1, slot = k_first > 0 ? 0 : 1;
                     if (both) wait(&S.sum_full[og], taken & 1, ok);
-                    const Seq s = seq_of(f.b);
-                    const bool ends = (flags & kEnds) != 0, complete = k_first == 0 && ends;
-                    const int slot = k_first > 0 ? 0 : 1;
                     float *rec = p.part + static_cast<int64_t>(2 * c + slot) * rec_floats(R);
-                    const float *src = reinterpret_cast<const float *>(pbuf + og * Sh::kPBytes) + me;
-#pragma unroll
-                    for (int q = 0; q < kRW; ++q) {
-                        const int r = r0 + q, rw = R * f.rt + r;
-                        if (rw < s.rows) {
-                            float m = reinterpret_cast<const float *>(S.m[g])[r], zz = zrow(r), t = o[q];
-                            if (both) {
-                                const float m1 = reinterpret_cast<const float *>(S.sum_m[og])[r], M = fmaxf(m, m1);
-                                const float ref = M == -INFINITY ? 0.0f : M, a0 = ex2(m - ref), a1 = ex2(m1 - ref);
-                                zz = zz * a0 + S.sum_z[og][r] * a1;
-                                t = t * a0 + src[r * kPD] * a1;
-                                m = M;
-                            }
-                            if (complete) {
-                                const int ri = p.by_gq.quot(rw);
-                                p.out[static_cast<int64_t>(s.start + ri) * p.ldo + (f.head * p.GQ + rw - ri * p.GQ) * kPD + me] =
-                                    zz > 0.0f ? t / zz : 0.0f;
-                            } else {
-                                rec[r * kPD + me] = t;
-                                if (me == 0) *reinterpret_cast<float2 *>(rec + R * kPD + 2 * r) = make_float2(m, zz);
-                            }
+                    if (gt < R) {
+                        // factors of the two parts, the final division included
+                        const float m0 = reinterpret_cast<const float *>(S.m[g])[gt], m1 = both ? S.sum_m[og][gt] : -INFINITY;
+                        const float M = fmaxf(m0, m1), ref = M == -INFINITY ? 0.0f : M;
+                        float2 fac = make_float2(ex2(m0 - ref), ex2(m1 - ref));
+                        const float zz = zr * fac.x + (both ? S.sum_z[og][gt] * fac.y : 0.0f);
+                        if (complete) {
+                            const float iz = recip(zz);
+                            fac = make_float2(fac.x * iz, fac.y * iz);
+                        } else {
+                            *reinterpret_cast<float2 *>(rec + R * kPD + 2 * gt) = make_float2(M, zz);
                         }
+                        S.factors[g][gt] = fac;
+                    }
+                    any_of<kGroup>(false, g);
+                    const Seq s = f.s;
+                    const int rows = min(kRW, s.rows - R * f.rt - r0);
+                    const float *other = reinterpret_cast<const float *>(pbuf + og * Sh::kPBytes) + me;
+#pragma unroll 2
+                    for (int r = r0; r < r0 + rows; ++r) {
+                        const float2 fac = S.factors[g][r];
+                        float t = own[r * kPD] * fac.x;
+                        if (both) t = fmaf(other[r * kPD], fac.y, t);
+                        const int rw = R * f.rt + r, ri = p.by_gq.quot(rw);
+                        float *dst = complete ? p.out + static_cast<int64_t>(s.start + ri) * p.ldo +
+                                                    (f.head * p.GQ + rw - ri * p.GQ) * kPD
+                                              : rec + r * kPD;
+                        dst[me] = t;
                     }
                     if (both) {
                         __syncwarp();
@@ -677,7 +750,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                         Piece pc;
                         pc.valid = 1;
                         pc.ends = ends;
-                        pc.b = f.b;
+                        pc.s = s;
                         pc.head = f.head;
                         pc.rt = f.rt;
                         pc.units = f.units;
@@ -695,7 +768,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
     if (warp == Sh::kWarpQK) tmem_dealloc(tmem, Sh::kTmemCols);
     const Piece pieces[2] = {S.piece[0], S.piece[1]};
     const bool cut[2] = {pieces[0].valid != 0, pieces[1].valid != 0};
-    merge_cut_items<R, Sh::kThreads>(p, cut, pieces, ranges, 1, S.last, seq_of);
+    merge_cut_items<R, Sh::kThreads>(p, cut, pieces, ranges, 1, S.last);
     pdl_launch_dependents();
 }
 
