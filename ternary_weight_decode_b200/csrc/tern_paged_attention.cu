@@ -78,11 +78,6 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = as_u32(__floats2half2_rn(x - f.x, y - f.y));
 }
 
-__device__ __noinline__ void wait_slow(uint64_t *bar, uint32_t parity) { mbar_wait_bounded(bar, parity); }
-__device__ __forceinline__ void wait_landed(uint64_t *bar, uint32_t parity) {
-    if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity);
-}
-
 // Codes c0 c1 (low half of the pair's bytes) as fp16 x 2.  int8: 1024 + (c +
 // 128) has the code's bits as its low byte (fp16 spacing 1 there), and one
 // subtraction leaves c; the caller has flipped the sign bits.  e4m3: the
@@ -120,6 +115,14 @@ struct __align__(16) TileInfo {
     int k;           // tile of the item, times 2, + 1 for the item's last tile
 };
 
+// A warp's piece of an item that others share.
+struct Piece {
+    int valid, ends;   // ends: holds the item's last tile
+    int head, rt, units;
+    Seq s;
+    long long u0;      // line index of the item's first tile
+};
+
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kPieceFloats = kRows * kPD;
 struct SplitShared {
@@ -129,6 +132,7 @@ struct SplitShared {
     Piece piece[kWarps][2];
     uint64_t bars[kWarps][kStages];
     LineShared<kThreads> line;
+    CutItem cut[2];
     int last[2];
 };
 constexpr size_t kSplitSmem = kRingBytes + sizeof(SplitShared) + 1024;
@@ -156,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         S.piece[warp][0].valid = S.piece[warp][1].valid = 0;
         S.piece[warp][0].ends = 0;
+        if (warp < 2) S.cut[warp].valid = 0;
     }
     pdl_wait();
 
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int n = 0; n < 16; ++n) st.o[n] = make_float2(0.0f, 0.0f);
             }
             if (x.bi >= 0) {
-                wait_landed(&S.bars[warp][stage], (phases >> stage) & 1u);
+                mbar_wait_bounded(&S.bars[warp][stage], (phases >> stage) & 1u);
                 phases ^= 1u << stage;
                 const uint8_t *kt = my_ring + stage * kStageBytes, *vt = kt + kTileBytes;
                 // scores: tokens j0 + 2t, + 1 (n = 0) and j0 + 8 + 2t, + 1 (n = 1) of row g
@@ -410,8 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- pieces of this CTA's warps: group a begins with a warp's last piece
     // (a = warp) or with the first piece of warp 0 (a = -1), and goes on with
     // the first pieces of the warps behind it until the item ends
-    bool cut[2] = {false, false};  // groups that other CTAs share: begun before this CTA, going on behind it
-    Piece shared_piece[2] = {};
     const bool is_warp = lane < kWarps;
     const unsigned first_ok = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].valid);
     const unsigned first_ends = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].ends);
@@ -430,10 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w1 += ends ? e : run;
         }
         const bool complete = a >= 0 && ends;
-        if (!complete) {
-            if (slot0 == 0) cut[0] = true; else cut[1] = true;
-            if (slot0 == 0) shared_piece[0] = pc; else shared_piece[1] = pc;
-        }
+        if (!complete && tid == 0) note_cut(S.cut[slot0], R, kWarps, pc.head, pc.rt, pc.s, pc.u0, pc.units);
         const Seq s = pc.s;
         for (int rr = warp; rr < kRows; rr += kWarps) {
             const int row = kRows * pc.rt + rr;
@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    merge_cut_items<kRows, kThreads>(p, cut, shared_piece, R, kWarps, S.last);
+    __syncthreads();
+    merge_cut_items<kRows, kThreads>(p, S.cut, S.last, nullptr);
     pdl_launch_dependents();
 }
 

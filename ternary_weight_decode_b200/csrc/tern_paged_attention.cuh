@@ -256,60 +256,67 @@ __device__ __forceinline__ void add_scaled(float4 &o, float &z, float f, float4 
     o.w = fmaf(f, x.w, o.w);
 }
 
-// A piece of a cut item.
-struct Piece {
-    int valid, ends;   // ends: holds the item's last tile
-    int head, rt, units;
+// An item that the CTA shares with others: its range begins inside item 0
+// (record in slot 2c), or ends inside item 1, which began in it (slot 2c + 1;
+// the middle CTAs of an item have slot 2c alone).
+struct CutItem {
+    int valid;
+    int head, rt;
     Seq s;
-    long long u0;      // line index of the item's first tile
+    int first, parts;  // the CTA with the item's first part, and how many have one
 };
 
-constexpr int kMergeParts = 10;
+// item: the CTA's first (a = 0) or last (a = 1) item, whose first tile has line
+// index u0.
+__device__ __forceinline__ void note_cut(CutItem &x, const Ranges &ranges, int per_cta, int head, int rt, const Seq &s,
+                                         long long u0, int units) {
+    x.head = head;
+    x.rt = rt;
+    x.s = s;
+    x.first = ranges.owner(u0) / per_cta;
+    x.parts = ranges.owner(u0 + units - 1) / per_cta - x.first + 1;
+    x.valid = 1;
+}
 
-// Items cut between CTAs: cut[0]: the CTA's range begins inside pc[0], whose
-// record lies in slot 2c; cut[1]: it ends inside pc[1] (slot 2c + 1; the
-// middle CTAs of an item have slot 2c alone).  Whoever finishes an item's last
-// part merges all of them in range order.  All threads of the CTA, after
-// their writes of the records; per_cta: ranges of the line in one CTA.
+constexpr int kMergeParts = 10;  // records that a warp has in flight
+
+// Items cut between CTAs: whoever finishes an item's last part merges all of
+// them, in range order.  All threads of the CTA, after its records have been
+// written and a __syncthreads; scratch: shared memory, R * (kPD + 4) floats, 16-byte aligned.
 template <int R, int NT>
-__device__ __forceinline__ void merge_cut_items(const AttnParams &p, const bool (&cut)[2], const Piece (&pc)[2],
-                                                const Ranges &ranges, int per_cta, int (&last)[2]) {
+__device__ __forceinline__ void merge_cut_items(const AttnParams &p, const CutItem (&cut)[2], int (&last)[2], float *scratch) {
+    constexpr int kSplit = NT / 32 >= 2 * R ? 2 : 1;  // warps of a row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (!cut[0] && !cut[1]) return;
-    __threadfence();
-    __syncthreads();
-    int first[2], parts[2];
-#pragma unroll 1
-    for (int a = 0; a < 2; ++a) {
-        first[a] = parts[a] = 0;
-        if (!cut[a]) continue;
-        first[a] = ranges.owner(pc[a].u0) / per_cta;
-        parts[a] = ranges.owner(pc[a].u0 + pc[a].units - 1) / per_cta - first[a] + 1;
-        if (tid == 32 * a) {
-            const int done = atomicAdd(p.counters + first[a], 1);
-            last[a] = done + 1 == parts[a];
-            if (done + 1 == parts[a]) p.counters[first[a]] = 0;  // zero at rest
-        }
+    if (!cut[0].valid && !cut[1].valid) return;
+    if (tid < 2 && cut[tid].valid) {
+        __threadfence();  // the CTA's records (ordered before this thread by the barrier) before its arrival
+        const int done = atomicAdd(p.counters + cut[tid].first, 1);
+        const int l = done + 1 == cut[tid].parts;
+        if (l) p.counters[cut[tid].first] = 0;  // zero at rest
+        __threadfence();
+        last[tid] = l;
     }
     __syncthreads();
 #pragma unroll 1
     for (int a = 0; a < 2; ++a) {
-        if (!cut[a] || !last[a]) continue;
-        __threadfence();
-        const Seq s = pc[a].s;
+        if (!cut[a].valid || !last[a]) continue;
+        const Seq s = cut[a].s;
+        const int parts = cut[a].parts, head = cut[a].head, rt = cut[a].rt;
         // part i's record: slot 2 first + 1 for the first, 2 (first + i) behind it
-        const float *base = p.part + static_cast<int64_t>(2 * first[a]) * rec_floats(R);
+        const float *base = p.part + static_cast<int64_t>(2 * cut[a].first) * rec_floats(R);
         auto offset = [](int i) { return (i == 0 ? 1 : 2 * i) * rec_floats(R); };
+        const int half = (parts + kSplit - 1) / kSplit, mine = kSplit == 1 ? 0 : warp / R;
+        const int begin = mine * half, end = min(parts, begin + half);
 #pragma unroll 1
-        for (int rr = warp; rr < R; rr += NT / 32) {
-            const int row = R * pc[a].rt + rr;
+        for (int rr = kSplit == 1 ? warp : warp % R; rr < R && mine < kSplit; rr += kSplit == 1 ? NT / 32 : R) {
+            const int row = R * rt + rr;
             if (row >= s.rows) break;
             const float *sums = base + rr * kPD + 4 * lane, *stats = base + R * kPD + 2 * rr;
             float z = 0.0f, M = -INFINITY;
             float4 o = make_float4(0, 0, 0, 0);
 #pragma unroll 1
-            for (int i0 = 0; i0 < parts[a]; i0 += kMergeParts) {  // so many at a time: their loads are all in flight at once
-                const int n = min(kMergeParts, parts[a] - i0);
+            for (int i0 = begin; i0 < end; i0 += kMergeParts) {
+                const int n = min(kMergeParts, end - i0);
                 float2 mz = make_float2(-INFINITY, 0.0f);
                 if (lane < n) mz = __ldcg(reinterpret_cast<const float2 *>(stats + offset(i0 + lane)));
                 float4 x[kMergeParts];
@@ -332,7 +339,25 @@ __device__ __forceinline__ void merge_cut_items(const AttnParams &p, const bool 
                     o.w = fmaf(fi, x[i].w, o.w);
                 }
             }
-            write_row(p, s.start, pc[a].head, row, o, z, 4 * lane);
+            if constexpr (kSplit == 2) {  // the second half's sums to the first half's warp
+                float *sc = scratch + rr * (kPD + 4);
+                if (mine == 1) {
+                    *reinterpret_cast<float4 *>(sc + 4 * lane) = o;
+                    if (lane == 0) *reinterpret_cast<float2 *>(sc + kPD) = make_float2(M, z);
+                }
+                asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + rr) : "memory");
+                if (mine == 0) {
+                    const float4 x = *reinterpret_cast<const float4 *>(sc + 4 * lane);
+                    const float2 mz = *reinterpret_cast<const float2 *>(sc + kPD);
+                    const float Mn = fmaxf(M, mz.x), ref = Mn == -INFINITY ? 0.0f : Mn, back = ex2(M - ref);
+                    o = make_float4(o.x * back, o.y * back, o.z * back, o.w * back);
+                    z *= back;
+                    add_scaled(o, z, ex2(mz.x - ref), x, mz.y);
+                }
+                asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + rr) : "memory");
+                if (mine == 1) continue;
+            }
+            write_row(p, s.start, head, row, o, z, 4 * lane);
         }
     }
 }

@@ -107,7 +107,7 @@ template <int R>
 struct TcShared {
     using Sh = Shape<R>;
     TileInfo info[kInfo];
-    ItemInfo item[kItems];
+    ItemInfo item[kItems], first_item;
     float4 rowf[kItems][R / 4];        // score scale of each row's digits
     float4 m[2][R / 4], mref[2][R / 4];  // each group's references; mref: 0 for a row that has seen nothing
     float4 back[2][R / 4];            // what new references make of the sums before
@@ -119,7 +119,7 @@ struct TcShared {
     uint64_t k_full[Sh::kStages], k_empty[Sh::kStages], v_full[Sh::kStages], v_empty[Sh::kStages];
     uint64_t info_full[kInfo], item_full[kItems], item_empty[kItems];
     uint64_t s_full[Sh::kSBufs], s_empty[Sh::kSBufs], p_full[2], p_empty[2], q_full[2], q_empty[2], sum_full[2], sum_empty[2];
-    Piece piece[2];
+    CutItem cut[2];
     uint32_t tmem;
     int accumulate[2];
     int last[2];
@@ -226,13 +226,16 @@ __device__ __forceinline__ void add_sums(uint32_t taddr, float vref, float (&o)[
 // infos of the items and tiles.
 template <int R, bool COPY_V, typename SeqOf>
 __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &maps, TcShared<R> &S, uint8_t *kring,
-                                          uint8_t *vring, const Line &L, long long u0, int count, SeqOf seq_of) {
+                                          uint8_t *vring, const Line &L, const Ranges &ranges, long long u0, int count,
+                                          SeqOf seq_of) {
     constexpr int kSt = Shape<R>::kStages;
     const PagedView &v = p.v;
     const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
     bool ok = true;
     // four tiles at a time (lane = 8 * tile + block): a batch is looked up while the one before is copied
     Cursor<kTB> cur = find_place<R, kTB>(p, S.line, L, u0, seq_of);
+    const int k_first = cur.k;
+    if (lane == 0) S.first_item = {cur.head, cur.rt, cur.units(), cur.s};
     int step = sub, bi = -1, j0 = 0;
     float ks = 0.0f, vs = 0.0f;
 #pragma unroll 1
@@ -331,6 +334,14 @@ __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &
             }
         }
     }
+    // the items that other CTAs have parts of
+    if (lane == 0 && k_first > 0) {
+        const ItemInfo &it = S.first_item;
+        note_cut(S.cut[0], ranges, 1, it.head, it.rt, it.s, u0 - k_first, it.tiles);
+    }
+    // (the last tile's item, as the lane that looked it up has it: cut if it goes on and began in this range)
+    if (j == 0 && sub == (count - 1) % 4 && cur.k + 1 < cur.units() && cur.k <= count - 1)
+        note_cut(S.cut[1], ranges, 1, cur.head, cur.rt, cur.s, u0 + count - 1 - cur.k, cur.units());
     // no copy is in flight when the CTA ends, even after a wait that ran out
     bool land = true;
 #pragma unroll 1
@@ -396,7 +407,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             mbar_init(&S.q_empty[i], 1);
             mbar_init(&S.sum_full[i], 4 * Sh::kHalves);
             mbar_init(&S.sum_empty[i], 4 * Sh::kHalves);
-            S.piece[i].valid = 0;
+            S.cut[i].valid = 0;
         }
         for (int i = 0; i < kInfo; ++i) mbar_init(&S.info_full[i], 1);
         for (int i = 0; i < kItems; ++i) {
@@ -430,7 +441,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
     if (count == 0) {
     } else if (warp == Sh::kWarpK) {
         auto seq_of = [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); };
-        copy_keys<R, (Sh::kWarpV < 0)>(p, maps, S, kring, vring, L, u0, count, seq_of);
+        copy_keys<R, (Sh::kWarpV < 0)>(p, maps, S, kring, vring, L, ranges, u0, count, seq_of);
     } else if (warp == Sh::kWarpV) {
         copy_values<R>(maps, S, vring, count);
     } else if (warp == Sh::kWarpQK) {
@@ -746,17 +757,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                         if (lane == 0) mbar_arrive(&S.sum_empty[og]);
                         ++taken;
                     }
-                    if (!complete && gt == 0) {
-                        Piece pc;
-                        pc.valid = 1;
-                        pc.ends = ends;
-                        pc.s = s;
-                        pc.head = f.head;
-                        pc.rt = f.rt;
-                        pc.units = f.units;
-                        pc.u0 = u0 + i - f.k;
-                        S.piece[slot] = pc;
-                    }
                 }
                 any_of<kGroup>(false, g);  // the sums have been read
             }
@@ -766,9 +766,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     if (warp == Sh::kWarpQK) tmem_dealloc(tmem, Sh::kTmemCols);
-    const Piece pieces[2] = {S.piece[0], S.piece[1]};
-    const bool cut[2] = {pieces[0].valid != 0, pieces[1].valid != 0};
-    merge_cut_items<R, Sh::kThreads>(p, cut, pieces, ranges, 1, S.last);
+    merge_cut_items<R, Sh::kThreads>(p, S.cut, S.last, reinterpret_cast<float *>(pbuf));
     pdl_launch_dependents();
 }
 
