@@ -561,29 +561,72 @@ def tern_attention_decode_q4_0(q: torch.Tensor, cache: KVCache, L: int, out: tor
 
 
 # ------------------------------------------------------------------ rotary embedding, paged KV cache
-def _here(*tensors) -> None:
-    """The call runs on the current device: every buffer has to be there."""
+# The calls below run once per layer and token, so they cost the host little:
+# the descriptors' structs are made and checked once (again when a field is
+# replaced), and each call checks its tensors with a few cheap queries.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+class _Described:
+    """A descriptor whose C struct is kept until one of its fields is replaced."""
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_kept", None)
+
+    def described(self):
+        """(address of the struct, device index)"""
+        kept = self.__dict__.get("_kept")
+        if kept is None:
+            s = self.struct()
+            kept = (ctypes.addressof(s), self.device_index(), s)
+            self.__dict__["_kept"] = kept
+        return kept
+
+
+def _one_device(*tensors) -> int:
+    dev = {t.get_device() for t in tensors}
+    if len(dev) != 1 or -1 in dev:
+        raise ValueError(f"the buffers must be on one CUDA device: {sorted(dev)}")
+    return dev.pop()
+
+
+def _call_stream(dev: int, stream) -> int:
+    """The raw stream of a call on device `dev`, which has to be the current one."""
     cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != cur):
-            raise ValueError(f"a buffer is on {t.device}, the current device is cuda:{cur}")
+    if dev != cur:
+        raise ValueError(f"the buffers are on cuda:{dev}, the current device is cuda:{cur}")
+    return _raw_stream(cur) if stream is None else stream.cuda_stream
 
 
-def _heads(t: torch.Tensor, D: int | None = None) -> int:
-    """The row stride of fp32 rows of heads, a tensor or view [T, H, D]."""
-    assert t.dtype == torch.float32 and t.dim() == 3 and (D is None or t.shape[2] == D)
-    T, H, d = t.shape
-    assert (t.stride(2) == 1 or d == 1) and (t.stride(1) == d or H == 1), "heads of a row must be contiguous"
-    return t.stride(0) if T > 1 else max(H * d, 1)
+def _heads(t: torch.Tensor, dev: int, T: int, H: int, D: int) -> int:
+    """The row stride of fp32 rows of heads, a tensor or view [T, H, D] on device `dev`."""
+    if t.get_device() != dev:
+        raise ValueError(f"a buffer is on {t.device}, the others are on cuda:{dev}")
+    assert t.dtype == torch.float32 and t.shape == (T, H, D), (t.dtype, tuple(t.shape), (T, H, D))
+    st = t.stride()
+    assert st[2] == 1 and (st[1] == D or H == 1), "the heads of a row must be contiguous"
+    return st[0] if T > 1 else H * D
 
 
-def _i32(t: torch.Tensor, *shape) -> torch.Tensor:
-    assert t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape, (tuple(t.shape), shape)
-    return t
+def _positions(t: torch.Tensor, dev: int, axes: int, T: int) -> int:
+    if t.get_device() != dev:
+        raise ValueError(f"pos is on {t.device}, the others are on cuda:{dev}")
+    assert t.dtype == torch.int32 and t.shape == (axes, T) and t.is_contiguous(), (t.dtype, tuple(t.shape))
+    return t.data_ptr()
+
+
+def _counter(t: torch.Tensor | None, dev: int):
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"d_invalid is on {t.device}, the others are on cuda:{dev}")
+    assert t.dtype == torch.int32 and t.numel() >= 1
+    return t.data_ptr()
 
 
 @dataclass
-class RopePlan:
+class RopePlan(_Described):
     """A rotary embedding: `table` fp32 [n_pos, rot_dim/2, 2] of (cos, sin), and
     the pairs that each position axis turns (one axis, all pairs, by default)."""
     table: torch.Tensor
@@ -603,6 +646,9 @@ class RopePlan:
         tern_rope_table(theta, scale, table, stream)
         return RopePlan(table, sections, interleaved)
 
+    def device_index(self) -> int:
+        return _one_device(self.table)
+
     def struct(self) -> tern_rope_plan:
         t = self.table
         assert t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 3 and t.shape[2] == 2
@@ -617,24 +663,23 @@ class RopePlan:
 def tern_rope_table(theta: float, scale: float, table: torch.Tensor, stream=None):
     """Fills table fp32 [n_pos, rot_dim/2, 2] with the cosines and sines of the rotary angles."""
     assert table.dtype == torch.float32 and table.is_contiguous() and table.dim() == 3 and table.shape[2] == 2
-    _here(table)
-    _check(lib().tern_rope_table(theta, scale, 2 * table.shape[1], table.shape[0], _ptr(table), _stream(stream)),
-           "tern_rope_table")
+    _check(lib().tern_rope_table(theta, scale, 2 * table.shape[1], table.shape[0], table.data_ptr(),
+                                 _call_stream(_one_device(table), stream)), "tern_rope_table")
 
 
 def tern_rope(rope: RopePlan, pos: torch.Tensor, x: torch.Tensor, y: torch.Tensor, d_invalid=None, stream=None):
     """y [T, H, D] = x rotated by pos int32 [axes, T]; y may be x."""
     T, H, D = x.shape
-    assert y.shape == x.shape
-    _i32(pos, rope.axes, T)
-    _here(rope.table, pos, x, y, d_invalid)
-    r = rope.struct()
-    _check(lib().tern_rope(ctypes.addressof(r), pos.data_ptr(), T, H, D, x.data_ptr(), _heads(x), y.data_ptr(),
-                           _heads(y), _ptr(d_invalid), _stream(stream)), "tern_rope")
+    plan, dev, _ = rope.described()
+    st = (_lib or lib()).tern_rope(plan, _positions(pos, dev, rope.axes, T), T, H, D, x.data_ptr(),
+                                   _heads(x, dev, T, H, D), y.data_ptr(), _heads(y, dev, T, H, D),
+                                   _counter(d_invalid, dev), _call_stream(dev, stream))
+    if st:
+        _check(st, "tern_rope")
 
 
 @dataclass
-class PagedCache:
+class PagedCache(_Described):
     """A paged 8-bit KV cache of one layer: codes uint8 [n_pages, Hkv, page_size, D]
     and fp32 scales [n_pages, Hkv, page_size/16] for K and for V."""
     kind: int
@@ -655,6 +700,9 @@ class PagedCache:
             return torch.zeros((n_pages, Hkv, page_size // TERN_KV_BLOCK), dtype=torch.float32, device=device)
         return PagedCache(kind, Hkv, D, page_size, codes(), scales(), codes(), scales())
 
+    def device_index(self) -> int:
+        return _one_device(self.k_codes, self.k_scales, self.v_codes, self.v_scales)
+
     def struct(self) -> tern_paged_cache:
         n = self.k_codes.shape[0]
         for codes, scales in ((self.k_codes, self.k_scales), (self.v_codes, self.v_scales)):
@@ -666,7 +714,7 @@ class PagedCache:
 
 
 @dataclass
-class PagedBatch:
+class PagedBatch(_Described):
     """A batch over a paged cache (include/tern.h): row_start int32 [B + 1], ctx
     int32 [B], pages int32 [B, pages_ld], all on the device; T rows, at most
     about max_rows rows and max_ctx tokens a sequence."""
@@ -677,52 +725,61 @@ class PagedBatch:
     max_rows: int
     max_ctx: int
 
+    def device_index(self) -> int:
+        return _one_device(self.row_start, self.ctx, self.pages)
+
     def struct(self) -> tern_paged_batch:
         B = self.ctx.shape[0]
-        _i32(self.row_start, B + 1)
-        _i32(self.ctx, B)
-        _i32(self.pages, B, self.pages.shape[1])
+        for t, shape in ((self.row_start, (B + 1,)), (self.ctx, (B,)), (self.pages, (B, self.pages.shape[1]))):
+            assert t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape, (t.dtype, tuple(t.shape))
         return tern_paged_batch(B, self.T, self.max_rows, self.max_ctx, self.row_start.data_ptr(),
                                 self.ctx.data_ptr(), self.pages.data_ptr(), self.pages.shape[1], 0)
 
-    def here(self, cache: PagedCache, *tensors) -> None:
-        _here(self.row_start, self.ctx, self.pages, cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales,
-              *tensors)
+
+def _batch_and_cache(batch: PagedBatch, cache: PagedCache):
+    b, dev, _ = batch.described()
+    c, dev_c, _ = cache.described()
+    if dev != dev_c:
+        raise ValueError(f"the batch is on cuda:{dev}, the cache on cuda:{dev_c}")
+    return b, c, dev
 
 
 def tern_kv_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, rope: RopePlan,
                          batch: PagedBatch, cache: PagedCache, q_out: torch.Tensor, d_invalid=None, stream=None):
     """q_out [T, Hq, D] = q rotated; k (rotated) and v [T, Hkv, D] quantised into the cache.
     pos int32 [axes, T]; q_out may be q."""
-    T, Hq, D = q.shape
-    assert q_out.shape == q.shape and T == batch.T and D == cache.D
-    assert tuple(k.shape) == (T, cache.Hkv, D) and v.shape == k.shape
-    _i32(pos, rope.axes, T)
-    batch.here(cache, rope.table, pos, q, k, v, q_out, d_invalid)
-    r, b, c = rope.struct(), batch.struct(), cache.struct()
-    _check(lib().tern_kv_append_paged(q.data_ptr(), _heads(q), Hq, k.data_ptr(), _heads(k), v.data_ptr(), _heads(v),
-                                      pos.data_ptr(), ctypes.addressof(r), ctypes.addressof(b), ctypes.addressof(c),
-                                      q_out.data_ptr(), _heads(q_out), _ptr(d_invalid), _stream(stream)),
-           "tern_kv_append_paged")
+    T, Hq, Hkv, D = batch.T, q.shape[1], cache.Hkv, cache.D
+    b, c, dev = _batch_and_cache(batch, cache)
+    plan, dev_r, _ = rope.described()
+    if dev_r != dev:
+        raise ValueError(f"the rotary table is on cuda:{dev_r}, the batch on cuda:{dev}")
+    st = (_lib or lib()).tern_kv_append_paged(
+        q.data_ptr(), _heads(q, dev, T, Hq, D), Hq, k.data_ptr(), _heads(k, dev, T, Hkv, D), v.data_ptr(),
+        _heads(v, dev, T, Hkv, D), _positions(pos, dev, rope.axes, T), plan, b, c, q_out.data_ptr(),
+        _heads(q_out, dev, T, Hq, D), _counter(d_invalid, dev), _call_stream(dev, stream))
+    if st:
+        _check(st, "tern_kv_append_paged")
 
 
 def tern_kv_read_paged(batch: PagedBatch, cache: PagedCache, k_out: torch.Tensor, v_out: torch.Tensor,
                        d_invalid=None, stream=None):
     """k_out, v_out [T, Hkv, D] = the cache's values of the batch's rows."""
-    assert tuple(k_out.shape) == (batch.T, cache.Hkv, cache.D) and v_out.shape == k_out.shape
-    batch.here(cache, k_out, v_out, d_invalid)
-    b, c = batch.struct(), cache.struct()
-    _check(lib().tern_kv_read_paged(ctypes.addressof(b), ctypes.addressof(c), k_out.data_ptr(), _heads(k_out),
-                                    v_out.data_ptr(), _heads(v_out), _ptr(d_invalid), _stream(stream)),
-           "tern_kv_read_paged")
+    b, c, dev = _batch_and_cache(batch, cache)
+    T, H, D = batch.T, cache.Hkv, cache.D
+    st = (_lib or lib()).tern_kv_read_paged(b, c, k_out.data_ptr(), _heads(k_out, dev, T, H, D), v_out.data_ptr(),
+                                            _heads(v_out, dev, T, H, D), _counter(d_invalid, dev),
+                                            _call_stream(dev, stream))
+    if st:
+        _check(st, "tern_kv_read_paged")
 
 
 def tern_attention_paged_workspace_bytes(Hq: int, cache: PagedCache) -> int:
-    b = ctypes.c_size_t()
-    c = cache.struct()
-    _check(lib().tern_attention_paged_workspace_bytes(Hq, ctypes.addressof(c), ctypes.byref(b)),
+    n = ctypes.c_size_t()
+    c, dev, _ = cache.described()
+    _call_stream(dev, None)  # (the answer is the current device's)
+    _check(lib().tern_attention_paged_workspace_bytes(Hq, c, ctypes.byref(n)),
            "tern_attention_paged_workspace_bytes")
-    return b.value
+    return n.value
 
 
 def attention_paged_workspace(Hq: int, cache: PagedCache) -> torch.Tensor:
@@ -737,14 +794,17 @@ def tern_attention_paged(q: torch.Tensor, batch: PagedBatch, cache: PagedCache, 
                          stream=None):
     """out [T, Hq, D] = causal attention of the batch's rows q over the cache;
     window tokens (0: all) and the first `sinks` are visible; scale 1/sqrt(D) by default."""
-    T, Hq, D = q.shape
-    assert out.shape == q.shape and T == batch.T and D == cache.D
-    batch.here(cache, q, out, workspace)
-    b, c = batch.struct(), cache.struct()
-    _check(lib().tern_attention_paged(q.data_ptr(), _heads(q), Hq, ctypes.addressof(b), ctypes.addressof(c), window,
-                                      sinks, D ** -0.5 if scale is None else scale, out.data_ptr(), _heads(out),
-                                      workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                      _stream(stream)), "tern_attention_paged")
+    T, Hq, D = batch.T, q.shape[1], cache.D
+    b, c, dev = _batch_and_cache(batch, cache)
+    if workspace.get_device() != dev:
+        raise ValueError(f"the workspace is on {workspace.device}, the batch on cuda:{dev}")
+    assert workspace.is_contiguous()
+    st = (_lib or lib()).tern_attention_paged(
+        q.data_ptr(), _heads(q, dev, T, Hq, D), Hq, b, c, window, sinks, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), _heads(out, dev, T, Hq, D), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _call_stream(dev, stream))
+    if st:
+        _check(st, "tern_attention_paged")
 
 
 ENGINE_TENSOR_CORES, ENGINE_CUDA_CORES = 0, 1
