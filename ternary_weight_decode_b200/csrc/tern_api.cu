@@ -322,12 +322,9 @@ tern_status tern_kv_append_paged(const float *q, int32_t ldq, int32_t Hq, const 
     if (!good_rows(k, ldk, cache->Hkv, 128) || !good_rows(v, ldv, cache->Hkv, 128))
         return fail(TERN_EINVAL, "%s: k and v must be 16-byte aligned with strides >= Hkv * D, multiples of 4", name);
     if (!pos || !aligned(pos, 4) || !aligned(d_invalid, 4)) return fail(TERN_EINVAL, "%s: bad pos or d_invalid", name);
-    int sms = 0;
-    cudaError_t e = device_sms(&sms);
-    if (e != cudaSuccess) return cuda_status(e, name);
     tern::AppendLaunch A = {q,     k,      v,      ldq,   ldk, ldv, Hq, pos,
                             *rope, *batch, *cache, q_out, ldqo, d_invalid};
-    return cuda_status(tern::launch_kv_append_paged(A, sms, static_cast<cudaStream_t>(stream)), name);
+    return cuda_status(tern::launch_kv_append_paged(A, static_cast<cudaStream_t>(stream)), name);
 }
 
 tern_status tern_kv_read_paged(const tern_paged_batch *batch, const tern_paged_cache *cache, float *k_out, int32_t ldk,

@@ -117,7 +117,7 @@ struct AppendLaunch {
 cudaError_t launch_rope_table(double theta, double scale, int rot_dim, int n_pos, float *table, cudaStream_t s);
 cudaError_t launch_rope(const tern_rope_plan &R, const int32_t *pos, int T, int H, int D, const float *x, int ldx,
                         float *y, int ldy, int32_t *d_invalid, cudaStream_t s);
-cudaError_t launch_kv_append_paged(const AppendLaunch &A, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_append_paged(const AppendLaunch &A, cudaStream_t s);
 cudaError_t launch_kv_read_paged(const tern_paged_batch &B, const tern_paged_cache &C, float *k_out, int ldk,
                                  float *v_out, int ldv, int32_t *d_invalid, cudaStream_t s);
 struct PagedAttentionLaunch {
