@@ -131,7 +131,7 @@ struct SplitShared {
     float m[kWarps][2][kRows], z[kWarps][2][kRows];
     Piece piece[kWarps][2];
     uint64_t bars[kWarps][kStages];
-    LineShared<kThreads> line;
+    LineShared line;
     CutItem cut[2];
     int last[2];
 };

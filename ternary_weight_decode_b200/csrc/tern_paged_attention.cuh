@@ -158,60 +158,64 @@ __device__ __forceinline__ void advance(const AttnParams &p, Cursor<TB> &x, int 
     }
 }
 
-// The line of a launch, as a CTA of NT threads finds it.
-template <int NT>
+// The line of a launch, as a CTA finds it: its first kLineThreads threads share
+// out the sequences.
+constexpr int kLineThreads = 256;
 struct LineShared {
-    long long chunk[NT];  // line index where each thread's sequences begin
-    long long scan[NT / 32];
-    Seq seq[NT];          // the sequences, when each thread has one at most
+    long long chunk[kLineThreads];  // line index where each thread's sequences begin
+    long long scan[kLineThreads / 32];
+    Seq seq[kLineThreads];          // the sequences, when each thread has one at most
 };
 struct Line {
     long long total;
     int per;  // sequences of a thread
 };
 
-template <int R, int TB, int NT>
-__device__ __forceinline__ Line make_line(const AttnParams &p, LineShared<NT> &S) {
+// (All threads of the CTA, at least kLineThreads; holds two __syncthreads.)
+template <int R, int TB>
+__device__ __forceinline__ Line make_line(const AttnParams &p, LineShared &S) {
     const PagedView &v = p.v;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Line L;
-    L.per = (v.B + NT - 1) / NT;
-    long long mine = 0;
+    L.per = (v.B + kLineThreads - 1) / kLineThreads;
+    long long mine = 0, incl = 0;
+    if (warp < kLineThreads / 32) {
 #pragma unroll 1
-    for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b) {
-        const Seq s = sequence(p, b);
-        mine += v.Hkv * head_units<R, TB>(p, s);
-        S.seq[tid] = s;
-    }
-    long long incl = mine;
+        for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b) {
+            const Seq s = sequence(p, b);
+            mine += v.Hkv * head_units<R, TB>(p, s);
+            S.seq[tid] = s;
+        }
+        incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) S.scan[warp] = incl;
     }
-    if (lane == 31) S.scan[warp] = incl;
     __syncthreads();
     long long before = 0;
     L.total = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
+    for (int w = 0; w < kLineThreads / 32; ++w) {
         if (w < warp) before += S.scan[w];
         L.total += S.scan[w];
     }
-    S.chunk[tid] = before + incl - mine;
+    if (warp < kLineThreads / 32) S.chunk[tid] = before + incl - mine;
     __syncthreads();
     return L;
 }
 
 // The place of line index u < total (warp-collective).
-template <int R, int TB, int NT, typename SeqOf>
-__device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const LineShared<NT> &S, const Line &L, long long u,
+template <int R, int TB, typename SeqOf>
+__device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const LineShared &S, const Line &L, long long u,
                                                  SeqOf seq_of) {
     const int lane = threadIdx.x & 31;
     Cursor<TB> cur;
     int lo = 0;  // the last thread whose sequences begin at or before u
 #pragma unroll 1
-    for (int i = 0; i < NT / 32 && 32 * i * L.per < p.v.B; ++i) {
+    for (int i = 0; i < kLineThreads / 32 && 32 * i * L.per < p.v.B; ++i) {
         const unsigned le = __ballot_sync(0xffffffffu, S.chunk[32 * i + lane] <= u);
         if (le) lo = 32 * i + 31 - __clz(le);
     }

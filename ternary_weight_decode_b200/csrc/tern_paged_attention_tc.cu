@@ -67,9 +67,11 @@ struct Shape {
     static constexpr int kSBufs = R == 8 ? 4 : 2;     // S accumulators
     static constexpr int kNS = R == 8 ? 32 : 3 * R;   // columns of S: 3 per row, a multiple of 16
     static constexpr int kNP = 4 * R;                 // columns of O: the bytes of a token's row of weight digits
-    static constexpr int kStages = R == 8 ? 6 : 4;    // of K and of V
+    static constexpr int kStages = R == 8 ? 6 : 4;    // of K
+    static constexpr int kVStages = R == 8 ? 6 : 3;   // of V
     static constexpr int kQBytes = kNS * 128;
-    static constexpr int kPBytes = kTok * kNP;        // (also holds a group's R x 128 sums at the end of an item)
+    static constexpr int kPBytes = kTok * kNP;        // (also holds a group's own R x 128 sums at the end of an item)
+    static constexpr int kSumBytes = R * kPD * 4;     // the sums that one group hands to the other
     static constexpr uint32_t kTmemCols = R == 8 ? 256 : 512;
     static constexpr uint32_t kO = kSBufs * kNS;      // first column of O
     static_assert(kSBufs * kNS + 2 * kNP <= kTmemCols, "tensor memory");
@@ -113,12 +115,12 @@ struct TcShared {
     float4 back[2][R / 4];            // what new references make of the sums before
     float wmax[2][4][R];
     float zsum[2][4][R];
-    float sum_m[2][R], sum_z[2][R];   // a group's references and sums when it hands its part of an item over
+    float sum_m[R], sum_z[R];         // references and sums of the part of an item that a group hands to the other
     float2 factors[2][R];             // of the parts at an item's end
-    LineShared<Sh::kThreads> line;
-    uint64_t k_full[Sh::kStages], k_empty[Sh::kStages], v_full[Sh::kStages], v_empty[Sh::kStages];
+    LineShared line;
+    uint64_t k_full[Sh::kStages], k_empty[Sh::kStages], v_full[Sh::kVStages], v_empty[Sh::kVStages];
     uint64_t info_full[kInfo], item_full[kItems], item_empty[kItems];
-    uint64_t s_full[Sh::kSBufs], s_empty[Sh::kSBufs], p_full[2], p_empty[2], q_full[2], q_empty[2], sum_full[2], sum_empty[2];
+    uint64_t s_full[Sh::kSBufs], s_empty[Sh::kSBufs], p_full[2], p_empty[2], q_full[2], q_empty[2], sum_full, sum_empty;
     CutItem cut[2];
     uint32_t tmem;
     int accumulate[2];
@@ -128,7 +130,8 @@ struct TcShared {
 template <int R>
 constexpr size_t tc_smem() {
     using Sh = Shape<R>;
-    return 2 * Sh::kStages * kTileBytes + 2 * Sh::kPBytes + 2 * Sh::kQBytes + sizeof(TcShared<R>) + 1024;
+    return (Sh::kStages + Sh::kVStages) * kTileBytes + 2 * Sh::kPBytes + 2 * Sh::kQBytes + Sh::kSumBytes +
+           sizeof(TcShared<R>) + 1024;
 }
 static_assert(tc_smem<8>() <= 227 * 1024 && tc_smem<32>() <= 227 * 1024, "shared memory of one CTA");
 
@@ -228,7 +231,7 @@ template <int R, bool COPY_V, typename SeqOf>
 __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &maps, TcShared<R> &S, uint8_t *kring,
                                           uint8_t *vring, const Line &L, const Ranges &ranges, long long u0, int count,
                                           SeqOf seq_of) {
-    constexpr int kSt = Shape<R>::kStages;
+    constexpr int kSt = Shape<R>::kStages, kVSt = Shape<R>::kVStages;
     const PagedView &v = p.v;
     const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
     bool ok = true;
@@ -317,20 +320,21 @@ __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &
                 }
             }
             const uint32_t bytes = __popc(there >> (8 * e) & 255) * kPB * kPD;
-            const int at = stage * kTileBytes + j * kPB * kPD;
+            const int at = j * kPB * kPD;
             __syncwarp();
             if (lane == 8 * e) {
                 mbar_arrive_expect_tx(&S.k_full[stage], bytes);
                 mbar_arrive(&S.info_full[i % kInfo]);
             }
             __syncwarp();
-            if (sub == e && size >= 0) tma_load_2d_nohint(kring + at, &maps.k[size], 0, b_now * kPB, &S.k_full[stage]);
+            if (sub == e && size >= 0) tma_load_2d_nohint(kring + stage * kTileBytes + at, &maps.k[size], 0, b_now * kPB, &S.k_full[stage]);
             if (COPY_V) {
-                wait(&S.v_empty[stage], ((i / kSt) + 1) & 1, ok);
-                if (lane == 8 * e) mbar_arrive_expect_tx(&S.v_full[stage], bytes);
+                const int vs = i % kVSt;
+                wait(&S.v_empty[vs], ((i / kVSt) + 1) & 1, ok);
+                if (lane == 8 * e) mbar_arrive_expect_tx(&S.v_full[vs], bytes);
                 __syncwarp();
                 if (sub == e && size >= 0)
-                    tma_load_2d_nohint(vring + at, &maps.v[size], 0, b_now * kPB, &S.v_full[stage]);
+                    tma_load_2d_nohint(vring + vs * kTileBytes + at, &maps.v[size], 0, b_now * kPB, &S.v_full[vs]);
             }
         }
     }
@@ -345,16 +349,16 @@ __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &
     // no copy is in flight when the CTA ends, even after a wait that ran out
     bool land = true;
 #pragma unroll 1
-    for (int i = max(0, count - kSt); i < count; ++i) {
-        wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
-        if (COPY_V) wait(&S.v_full[i % kSt], (i / kSt) & 1, land);
-    }
+    for (int i = max(0, count - kSt); i < count; ++i) wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
+    if (COPY_V)
+#pragma unroll 1
+        for (int i = max(0, count - kVSt); i < count; ++i) wait(&S.v_full[i % kVSt], (i / kVSt) & 1, land);
 }
 
 // V's copies, by the tiles' infos; lanes 0-7 a block each.
 template <int R>
 __device__ __forceinline__ void copy_values(const CacheMaps &maps, TcShared<R> &S, uint8_t *vring, int count) {
-    constexpr int kSt = Shape<R>::kStages;
+    constexpr int kSt = Shape<R>::kVStages;
     const int lane = threadIdx.x & 31;
     bool ok = true;
 #pragma unroll 1
@@ -382,9 +386,10 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *kring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *vring = kring + kSt * kTileBytes;
-    uint8_t *pbuf = vring + kSt * kTileBytes;
+    uint8_t *pbuf = vring + Sh::kVStages * kTileBytes;
     uint8_t *qbuf = pbuf + 2 * Sh::kPBytes;
-    TcShared<R> &S = *reinterpret_cast<TcShared<R> *>(qbuf + 2 * Sh::kQBytes);
+    float *handed = reinterpret_cast<float *>(qbuf + 2 * Sh::kQBytes);
+    TcShared<R> &S = *reinterpret_cast<TcShared<R> *>(qbuf + 2 * Sh::kQBytes + Sh::kSumBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c = blockIdx.x;
     bool ok = true;
@@ -397,6 +402,8 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
         for (int i = 0; i < kSt; ++i) {
             mbar_init(&S.k_full[i], 1);
             mbar_init(&S.k_empty[i], 1);
+        }
+        for (int i = 0; i < Sh::kVStages; ++i) {
             mbar_init(&S.v_full[i], 1);
             mbar_init(&S.v_empty[i], 1);
         }
@@ -405,10 +412,10 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             mbar_init(&S.p_empty[i], 1);
             mbar_init(&S.q_full[i], 1);
             mbar_init(&S.q_empty[i], 1);
-            mbar_init(&S.sum_full[i], 4 * Sh::kHalves);
-            mbar_init(&S.sum_empty[i], 4 * Sh::kHalves);
             S.cut[i].valid = 0;
         }
+        mbar_init(&S.sum_full, 4 * Sh::kHalves);
+        mbar_init(&S.sum_empty, 4 * Sh::kHalves);
         for (int i = 0; i < kInfo; ++i) mbar_init(&S.info_full[i], 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&S.item_full[i], 1);
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
     }
     pdl_wait();
     tc_fence_before_sync();
-    const Line L = make_line<R, kTB>(p, S.line);  // (holds two __syncthreads)
+    const Line L = make_line<R, kTB>(p, S.line);
     tc_fence_after_sync();
     const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), L.total));
     Ranges ranges = {0, 0};
@@ -477,8 +484,8 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             constexpr uint32_t id_o = idesc_i8(128, Sh::kNP, 1, 0) | (1u << 15) | (1u << 16);  // both operands M/N-major
 #pragma unroll 1
             for (int i = 0; i < count; ++i) {
-                const int stage = i % kSt, g = i & 1;
-                wait(&S.v_full[stage], (i / kSt) & 1, ok);
+                const int stage = i % Sh::kVStages, g = i & 1;
+                wait(&S.v_full[stage], (i / Sh::kVStages) & 1, ok);
                 wait(&S.p_full[g], (i >> 1) & 1, ok);
                 tc_fence_after_sync();
                 const uint32_t a = smem_u32(vring + stage * kTileBytes), b = smem_u32(pbuf + g * Sh::kPBytes);
@@ -565,7 +572,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
         float z[kRW], o[kRW];
         float vref = 1.0f, inv_vref = 1.0f;
         int chain = 0, k_first = 0;
-        int given = 0, taken = 0;  // items handed to the other group, and taken from it
+        int handovers = 0;  // items of which both groups had parts
 #pragma unroll 1
         for (int i = g; i < count; i += 2) {
             const TileInfo &f = S.info[i % kInfo];
@@ -675,7 +682,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             // weights and their digits
             const float up = f.vs[me >> 4] * inv_vref * 0x1p32f;
             wait(&S.p_empty[g], ((i >> 1) + 1) & 1, ok);  // PV of this group's last tile has read the buffer
-            if ((flags & kGroupFirst) && given > 0) wait(&S.sum_empty[g], (given - 1) & 1, ok);  // and the other group its sums
             uint8_t *row = my_p + me * Sh::kNP;
 #pragma unroll
             for (int h = 0; h < kRW / 4; ++h) {
@@ -703,32 +709,33 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                 add_sums<kRW>(to, vref, o);
                 tc_fence_before_sync();
                 chain = 0;
-                // the sums, by dimension, where the weights lay
-                float *own = reinterpret_cast<float *>(my_p) + me;
+                // the sums by dimension: where the weights lay, or, when the other group has the item's last tile, handed
+                // over to it once it has taken what it was handed before
+                const bool hand = !(flags & kLast);
+                if (hand) wait(&S.sum_empty, (handovers + 1) & 1, ok);
+                float *own = (hand ? handed : reinterpret_cast<float *>(my_p)) + me;
 #pragma unroll
                 for (int r = 0; r < kRW; ++r) own[(r0 + r) * kPD] = o[r];
                 any_of<kGroup>(false, g);
                 const float zr = gt < R ? (S.zsum[g][0][gt] + S.zsum[g][1][gt]) + (S.zsum[g][2][gt] + S.zsum[g][3][gt]) : 0.0f;
-                if (!(flags & kLast)) {
-                    // the other group has the item's last tile: hand this part over
+                if (hand) {
                     if (gt < R) {
-                        S.sum_z[g][gt] = zr;
-                        S.sum_m[g][gt] = reinterpret_cast<const float *>(S.m[g])[gt];
+                        S.sum_z[gt] = zr;
+                        S.sum_m[gt] = reinterpret_cast<const float *>(S.m[g])[gt];
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&S.sum_full[g]);
-                    ++given;
+                    if (lane == 0) mbar_arrive(&S.sum_full);
                 } else {
                     const bool both = (flags & kBoth) != 0, ends = (flags & kEnds) != 0, complete = k_first == 0 && ends;
-                    const int og = g ^ 1, slot = k_first > 0 ? 0 : 1;
-                    if (both) wait(&S.sum_full[og], taken & 1, ok);
+                    const int slot = k_first > 0 ? 0 : 1;
+                    if (both) wait(&S.sum_full, handovers & 1, ok);
                     float *rec = p.part + static_cast<int64_t>(2 * c + slot) * rec_floats(R);
                     if (gt < R) {
                         // factors of the two parts, the final division included
-                        const float m0 = reinterpret_cast<const float *>(S.m[g])[gt], m1 = both ? S.sum_m[og][gt] : -INFINITY;
+                        const float m0 = reinterpret_cast<const float *>(S.m[g])[gt], m1 = both ? S.sum_m[gt] : -INFINITY;
                         const float M = fmaxf(m0, m1), ref = M == -INFINITY ? 0.0f : M;
                         float2 fac = make_float2(ex2(m0 - ref), ex2(m1 - ref));
-                        const float zz = zr * fac.x + (both ? S.sum_z[og][gt] * fac.y : 0.0f);
+                        const float zz = zr * fac.x + (both ? S.sum_z[gt] * fac.y : 0.0f);
                         if (complete) {
                             const float iz = recip(zz);
                             fac = make_float2(fac.x * iz, fac.y * iz);
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                     any_of<kGroup>(false, g);
                     const Seq s = f.s;
                     const int rows = min(kRW, s.rows - R * f.rt - r0);
-                    const float *other = reinterpret_cast<const float *>(pbuf + og * Sh::kPBytes) + me;
+                    const float *other = handed + me;
 #pragma unroll 2
                     for (int r = r0; r < r0 + rows; ++r) {
                         const float2 fac = S.factors[g][r];
@@ -754,10 +761,10 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                     }
                     if (both) {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&S.sum_empty[og]);
-                        ++taken;
+                        if (lane == 0) mbar_arrive(&S.sum_empty);
                     }
                 }
+                if (flags & kBoth) ++handovers;
                 any_of<kGroup>(false, g);  // the sums have been read
             }
         }
