@@ -67,8 +67,8 @@ struct Shape {
     static constexpr int kSBufs = R == 8 ? 4 : 2;     // S accumulators
     static constexpr int kNS = R == 8 ? 32 : 3 * R;   // columns of S: 3 per row, a multiple of 16
     static constexpr int kNP = 4 * R;                 // columns of O: the bytes of a token's row of weight digits
-    static constexpr int kStages = R == 8 ? 6 : 4;    // of K
-    static constexpr int kVStages = R == 8 ? 6 : 3;   // of V
+    static constexpr int kStages = R == 8 ? 6 : 3;    // of K
+    static constexpr int kVStages = R == 8 ? 6 : 4;   // of V (held longer: until PV)
     static constexpr int kQBytes = kNS * 128;
     static constexpr int kPBytes = kTok * kNP;        // (also holds a group's own R x 128 sums at the end of an item)
     static constexpr int kSumBytes = R * kPD * 4;     // the sums that one group hands to the other
@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(w4) << 21;  // this warp's quarter of tensor memory
         const uint32_t ts = tmem + lanes + 3 * r0, to = tmem + lanes + Sh::kO + g * Sh::kNP + 4 * r0;
         uint8_t *my_p = pbuf + g * Sh::kPBytes;
-        float z[kRW], o[kRW];
+        float2 z[kRW / 2];
+        float o[kRW];
         float vref = 1.0f, inv_vref = 1.0f;
         int chain = 0, k_first = 0;
         int handovers = 0;  // items of which both groups had parts
@@ -583,7 +584,9 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             if (flags & kGroupFirst) {
                 k_first = f.k - ((flags & kFirst) ? 0 : 1);  // the first tile that the CTA has of the item
 #pragma unroll
-                for (int r = 0; r < kRW; ++r) z[r] = o[r] = 0.0f;
+                for (int r = 0; r < kRW; ++r) o[r] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kRW / 2; ++r) z[r] = make_float2(0.0f, 0.0f);
                 if (gt < R) {
                     reinterpret_cast<float *>(S.m[g])[gt] = -INFINITY;
                     reinterpret_cast<float *>(S.mref[g])[gt] = 0.0f;
@@ -663,14 +666,15 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                     reinterpret_cast<float *>(S.back[g])[gt] = back;
                 }
                 any_of<kGroup>(false, g);
+                if (!(flags & kGroupFirst)) {
 #pragma unroll
-                for (int h = 0; h < kRW / 4; ++h) {
-                    const float4 back = S.back[g][r0 / 4 + h];
-                    const float bk[4] = {back.x, back.y, back.z, back.w};
+                    for (int h = 0; h < kRW / 4; ++h) {
+                        const float4 back = S.back[g][r0 / 4 + h];
+                        const float bk[4] = {back.x, back.y, back.z, back.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        z[4 * h + e] *= bk[e];
-                        o[4 * h + e] *= bk[e];
+                        for (int e = 0; e < 4; ++e) o[4 * h + e] *= bk[e];
+                        z[2 * h] = __fmul2_rn(z[2 * h], make_float2(back.x, back.y));
+                        z[2 * h + 1] = __fmul2_rn(z[2 * h + 1], make_float2(back.z, back.w));
                     }
                 }
                 if (vmax > 0.0f) {
@@ -681,17 +685,20 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
             }
             // weights and their digits
             const float up = f.vs[me >> 4] * inv_vref * 0x1p32f;
+            const float2 up2 = make_float2(up, up);
             wait(&S.p_empty[g], ((i >> 1) + 1) & 1, ok);  // PV of this group's last tile has read the buffer
             uint8_t *row = my_p + me * Sh::kNP;
 #pragma unroll
             for (int h = 0; h < kRW / 4; ++h) {
                 const float4 m = S.mref[g][r0 / 4 + h];
-                const float w[4] = {ex2(x[4 * h] - m.x), ex2(x[4 * h + 1] - m.y), ex2(x[4 * h + 2] - m.z),
-                                    ex2(x[4 * h + 3] - m.w)};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[4 * h + e] += w[e];
+                const float2 x0 = __fadd2_rn(make_float2(x[4 * h], x[4 * h + 1]), make_float2(-m.x, -m.y));
+                const float2 x1 = __fadd2_rn(make_float2(x[4 * h + 2], x[4 * h + 3]), make_float2(-m.z, -m.w));
+                const float2 w0 = make_float2(ex2(x0.x), ex2(x0.y)), w1 = make_float2(ex2(x1.x), ex2(x1.y));
+                z[2 * h] = __fadd2_rn(z[2 * h], w0);
+                z[2 * h + 1] = __fadd2_rn(z[2 * h + 1], w1);
+                const float2 u0 = __fmul2_rn(w0, up2), u1 = __fmul2_rn(w1, up2);
                 *reinterpret_cast<uint4 *>(row + (weights_chunk<R>(r0 / 4 + h, me) << 4)) =
-                    make_uint4(to_u32_sat(w[0] * up), to_u32_sat(w[1] * up), to_u32_sat(w[2] * up), to_u32_sat(w[3] * up));
+                    make_uint4(to_u32_sat(u0.x), to_u32_sat(u0.y), to_u32_sat(u1.x), to_u32_sat(u1.y));
             }
             if (gt == 0) S.accumulate[g] = chain > 0;
             ++chain;
@@ -702,7 +709,13 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
 
             if (flags & kGroupLast) {
                 // ---- this group's part of the item is done
-                const float zw = sum_rows<kRW>(z, lane);
+                float zs[kRW];
+#pragma unroll
+                for (int r = 0; r < kRW / 2; ++r) {
+                    zs[2 * r] = z[r].x;
+                    zs[2 * r + 1] = z[r].y;
+                }
+                const float zw = sum_rows<kRW>(zs, lane);
                 if (lane < kRW) S.zsum[g][w4][r0 + lane] = zw;
                 wait(&S.p_empty[g], (i >> 1) & 1, ok);
                 tc_fence_after_sync();
@@ -746,18 +759,25 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, 1)
                     }
                     any_of<kGroup>(false, g);
                     const Seq s = f.s;
-                    const int rows = min(kRW, s.rows - R * f.rt - r0);
-                    const float *other = handed + me;
+                    const int rows = min(R, s.rows - R * f.rt);
+                    // a warp a row, four dimensions a lane
+                    const float4 *mine = reinterpret_cast<const float4 *>(my_p) + lane;
+                    const float4 *other = reinterpret_cast<const float4 *>(handed) + lane;
 #pragma unroll 2
-                    for (int r = r0; r < r0 + rows; ++r) {
+                    for (int r = gt >> 5; r < rows; r += kGroup / 32) {
                         const float2 fac = S.factors[g][r];
-                        float t = own[r * kPD] * fac.x;
-                        if (both) t = fmaf(other[r * kPD], fac.y, t);
+                        float4 t = mine[r * (kPD / 4)];
+                        t = make_float4(t.x * fac.x, t.y * fac.x, t.z * fac.x, t.w * fac.x);
+                        if (both) {
+                            const float4 y = other[r * (kPD / 4)];
+                            t = make_float4(fmaf(y.x, fac.y, t.x), fmaf(y.y, fac.y, t.y), fmaf(y.z, fac.y, t.z),
+                                            fmaf(y.w, fac.y, t.w));
+                        }
                         const int rw = R * f.rt + r, ri = p.by_gq.quot(rw);
                         float *dst = complete ? p.out + static_cast<int64_t>(s.start + ri) * p.ldo +
                                                     (f.head * p.GQ + rw - ri * p.GQ) * kPD
                                               : rec + r * kPD;
-                        dst[me] = t;
+                        *reinterpret_cast<float4 *>(dst + 4 * lane) = t;
                     }
                     if (both) {
                         __syncwarp();
