@@ -321,17 +321,15 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int b, int b
         if (r < n) {
             int at[3];
             float c[4], s[4];
-            if (load_positions(p.R, p.pos, v.T, p.axes, row + r, at)) {
-                if (is_k) {
-                    load_turns(p.R, at, j, c, s);
-                    turn(p.R, j, a[i], c8[i], c, s);
-                }
-            } else {  // a row outside the table is appended as 0
-                ++bad;
+            const bool ok = load_positions(p.R, p.pos, v.T, p.axes, row + r, at);
+            if (!ok) {  // a row outside the table is appended as 0
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a[i][e] = c8[i][e] = 0.0f;
+            } else if (is_k) {
+                load_turns(p.R, at, j, c, s);
+                turn(p.R, j, a[i], c8[i], c, s);
             }
-            if (bi0 < 0 && i + 1 > bad) ++bad;
+            bad += !ok || bi0 < 0;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[i][e]), fabsf(c8[i][e])));

@@ -164,28 +164,50 @@ constexpr int kLineThreads = 256;
 struct LineShared {
     long long chunk[kLineThreads];  // line index where each thread's sequences begin
     long long scan[kLineThreads / 32];
-    Seq seq[kLineThreads];          // the sequences, when each thread has one at most
+    Seq seq[kLineThreads];          // with one sequence a thread at most: the sequences,
+    int head[kLineThreads];         // and the tiles of one KV head of each
 };
 struct Line {
     long long total;
     int per;  // sequences of a thread
 };
 
-// (All threads of the CTA, at least kLineThreads; holds two __syncthreads.)
+// (All threads of the CTA, at least kLineThreads; holds several __syncthreads.)
 template <int R, int TB>
 __device__ __forceinline__ Line make_line(const AttnParams &p, LineShared &S) {
     const PagedView &v = p.v;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool counts = tid < kLineThreads;
     Line L;
     L.per = (v.B + kLineThreads - 1) / kLineThreads;
+    Seq s = {0, 0, 0, 0};
+    if (counts && L.per == 1) {
+        if (tid < v.B) s = sequence(p, tid);
+        S.seq[tid] = s;
+    }
+    // sequences of many row tiles (prompts) are counted by a warp each, a row tile a lane
+    const bool many = __syncthreads_or(s.rows > 2 * R);
     long long mine = 0, incl = 0;
-    if (warp < kLineThreads / 32) {
+    if (counts && L.per > 1) {
 #pragma unroll 1
-        for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b) {
-            const Seq s = sequence(p, b);
-            mine += v.Hkv * head_units<R, TB>(p, s);
-            S.seq[tid] = s;
+        for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b)
+            mine += v.Hkv * head_units<R, TB>(p, sequence(p, b));
+    } else if (counts && !many) {
+        S.head[tid] = static_cast<int>(head_units<R, TB>(p, s));
+    } else if (counts) {
+#pragma unroll 1
+        for (int b = warp; b < v.B; b += kLineThreads / 32) {
+            const Seq t = S.seq[b];
+            int n = 0;
+#pragma unroll 1
+            for (int rt = lane; rt * R < t.rows; rt += 32) n += tile_count<TB>(tiles_of<R>(p, t, rt));
+            n = warp_sum_int(n);
+            if (lane == 0) S.head[b] = n;
         }
+    }
+    __syncthreads();
+    if (counts) {
+        if (L.per == 1 && tid < v.B) mine = static_cast<long long>(v.Hkv) * S.head[tid];
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -202,7 +224,7 @@ __device__ __forceinline__ Line make_line(const AttnParams &p, LineShared &S) {
         if (w < warp) before += S.scan[w];
         L.total += S.scan[w];
     }
-    if (warp < kLineThreads / 32) S.chunk[tid] = before + incl - mine;
+    if (counts) S.chunk[tid] = before + incl - mine;
     __syncthreads();
     return L;
 }
@@ -216,7 +238,7 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
     int lo = 0;  // the last thread whose sequences begin at or before u
 #pragma unroll 1
     for (int i = 0; i < kLineThreads / 32 && 32 * i * L.per < p.v.B; ++i) {
-        const unsigned le = __ballot_sync(0xffffffffu, S.chunk[32 * i + lane] <= u);
+        const unsigned le = __ballot_sync(0xffffffffu, S.chunk[32 * i + lane] <= u && (32 * i + lane) * L.per < p.v.B);
         if (le) lo = 32 * i + 31 - __clz(le);
     }
     long long off = u - S.chunk[lo], ph;
@@ -224,21 +246,33 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
 #pragma unroll 1
     for (;; ++b) {
         cur.s = seq_of(b);
-        ph = head_units<R, TB>(p, cur.s);
-        if (off < ph * p.v.Hkv) break;
+        ph = L.per == 1 ? S.head[b] : head_units<R, TB>(p, cur.s);
+        if (off < ph * p.v.Hkv || b + 1 == p.v.B) break;  // (the second: lengths that changed under the kernel end here)
         off -= ph * p.v.Hkv;
     }
     cur.b = b;
-    cur.head = static_cast<int>(quot(off, ph));
-    off -= cur.head * ph;
-    cur.rt = 0;
-    cur.tl = tiles_of<R>(p, cur.s, 0);
+    cur.head = min(static_cast<int>(quot(off, max(ph, 1LL))), p.v.Hkv - 1);
+    int k = static_cast<int>(off - cur.head * ph);
+    // the row tile, 32 at a time
 #pragma unroll 1
-    while (off >= cur.units()) {
-        off -= cur.units();
-        cur.tl = tiles_of<R>(p, cur.s, ++cur.rt);
+    for (int rt0 = 0;; rt0 += 32) {
+        const int rt = rt0 + lane, n = rt * R < cur.s.rows ? tile_count<TB>(tiles_of<R>(p, cur.s, rt)) : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, incl > k);
+        if (past || (rt0 + 32) * R >= cur.s.rows) {
+            const int l = past ? __ffs(past) - 1 : 0;
+            cur.rt = rt0 + l;
+            cur.k = k - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, n, l));
+            break;
+        }
+        k -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    cur.k = static_cast<int>(off);
+    cur.tl = tiles_of<R>(p, cur.s, cur.rt);
     cur.ord = 0;
     return cur;
 }

@@ -19,11 +19,18 @@ matrix evenly over the SMs.  The fused form with statistics ("fused") and
 the unfused form with separate act_quant_fwht launches ("unfused", 8 per
 layer) are kept for comparison and for M > 2.
 
-Attention and norms are not on this path (the pages give no detail); the
-attention output is stood in by the q projection, and a weightless RMSNorm
-before each block is folded into s_x only (TERN_QUANT_RMSNORM), which leaves
-every int8 code unchanged and keeps the residual stream bounded over 64
-layers.  Every step above runs in libtern's kernels.
+By default attention is not on this path (the pages give no detail) and its
+output is stood in by the q projection.  With ``attention="paged"`` it is: the
+M token rows are the next tokens of M sequences with an 8-bit paged KV cache
+(``PagedAttention`` below), and between steps 1 and 2 come
+
+  1a. tern_kv_append_paged(q, k, v of qkv)  -> q rotated, K and V into the cache
+  1b. tern_attention_paged(q)               -> the input of Wo
+
+Norms are not on this path; a weightless RMSNorm before each block is folded
+into s_x only (TERN_QUANT_RMSNORM), which leaves every int8 code unchanged and
+keeps the residual stream bounded over 64 layers.  Every step above runs in
+libtern's kernels.
 """
 from __future__ import annotations
 
@@ -66,6 +73,62 @@ def make_matrix(fmt: int, N: int, K: int, seed: int, stream: int, scratch: torch
 
 
 @dataclass
+class PagedAttention:
+    """Attention of the decode step over an 8-bit paged KV cache: its settings,
+    and (after ``build``) the caches, page table and lengths of M sequences.
+
+    ``ctx`` and ``pos`` live on the device and a step advances them, so that one
+    captured graph decodes token after token; ``max_ctx`` tokens of pages are
+    set aside for each sequence."""
+    max_ctx: int
+    kind: int = tern.TERN_KV_INT8
+    page_size: int = 64
+    window: int = 0
+    sinks: int = 0
+    theta: float = 1e6
+    head_dim: int = 128
+
+    def build(self, n_layers: int, M: int, hidden: int, qkv: int) -> "PagedAttention":
+        self.Hq = hidden // self.head_dim
+        self.Hkv = (qkv - hidden) // (2 * self.head_dim)
+        assert self.Hq * self.head_dim == hidden and (self.Hq + 2 * self.Hkv) * self.head_dim == qkv
+        per = -(-self.max_ctx // self.page_size)
+        pages = torch.arange(M * per, dtype=torch.int32, device="cuda").view(M, per)
+        self.ctx = torch.zeros(M, dtype=torch.int32, device="cuda")   # tokens of each sequence so far
+        self.pos = torch.full((1, M), -1, dtype=torch.int32, device="cuda")
+        rows = torch.arange(M + 1, dtype=torch.int32, device="cuda")
+        self.batch = tern.PagedBatch(rows, self.ctx, pages, M, 1, self.max_ctx)
+        self.rope = tern.RopePlan.build(self.theta, self.head_dim, self.max_ctx)
+        self.caches = [tern.PagedCache.empty(self.kind, self.Hkv, self.head_dim, self.page_size, M * per)
+                       for _ in range(n_layers)]
+        self.ws = tern.attention_paged_workspace(self.Hq, self.caches[0])
+        self.q = torch.zeros((M, self.Hq, self.head_dim), dtype=torch.float32, device="cuda")
+        self.out = torch.zeros((M, hidden), dtype=torch.float32, device="cuda")
+        self.refused = torch.zeros(1, dtype=torch.int32, device="cuda")  # tokens past max_ctx (not appended)
+        return self
+
+    def set_ctx(self, ctx) -> None:
+        """Sets the tokens that each sequence has (the next step appends behind them)."""
+        self.ctx.copy_(torch.as_tensor(ctx, dtype=torch.int32))
+        self.pos[0].copy_(self.ctx - 1)
+
+    def advance(self) -> None:
+        self.ctx.add_(1)
+        self.pos.add_(1)
+
+    def layer(self, l: int, qkv_out: torch.Tensor) -> torch.Tensor:
+        """The attention of layer l on the rows of its QKV projection -> [M, hidden]."""
+        M, D, q, kv = qkv_out.shape[0], self.head_dim, self.Hq * self.head_dim, self.Hkv * self.head_dim
+        parts = (qkv_out[:, :q].view(M, self.Hq, D), qkv_out[:, q:q + kv].view(M, self.Hkv, D),
+                 qkv_out[:, q + kv:q + 2 * kv].view(M, self.Hkv, D))
+        tern.tern_kv_append_paged(*parts, self.pos, self.rope, self.batch, self.caches[l], self.q,
+                                  d_invalid=self.refused)
+        tern.tern_attention_paged(self.q, self.batch, self.caches[l], self.out.view(M, self.Hq, D), self.ws,
+                                  window=self.window, sinks=self.sinks)
+        return self.out
+
+
+@dataclass
 class DecodeModel:
     fmt: int
     n_layers: int
@@ -74,6 +137,7 @@ class DecodeModel:
     qkv: int = QKV
     ffn: int = FFN
     mode: str = "streamed"  # "streamed" (M <= 2), "fused" or "unfused"
+    attention: PagedAttention | None = None  # None: stood in by the q projection
     layers: list = field(default_factory=list)
 
     @property
@@ -113,17 +177,25 @@ class DecodeModel:
         self.st_qkv = tern.stats_buffer(M, self.qkv)
         self.st_x1 = tern.stats_buffer(M, self.hidden)
         self.st_h = tern.stats_buffer(M, self.ffn)
+        if self.attention is not None:
+            self.attention.build(self.n_layers, M, self.hidden, self.qkv)
+            self.st_attn = tern.stats_buffer(M, self.hidden)
         return self
 
     def bytes_per_step(self) -> int:
         return self.n_layers * layer_bytes(self.fmt, self.hidden, self.qkv, self.ffn)
 
     def launches_per_step(self) -> int:
-        if self.mode == "streamed":
-            return 4 * self.n_layers
-        return 4 * self.n_layers + 1 if self.mode == "fused" else 8 * self.n_layers
+        n = {"streamed": 4 * self.n_layers, "fused": 4 * self.n_layers + 1, "unfused": 8 * self.n_layers}[self.mode]
+        if self.attention is not None:  # append and attention; the fused form also needs the output's statistics
+            n += (3 if self.mode == "fused" else 2) * self.n_layers
+        return n
 
-    def layer_step_streamed(self, L: Layer, keep=None):
+    def attend(self, l: int) -> torch.Tensor:
+        """The input of layer l's O projection, behind its QKV projection."""
+        return self.qkv_out[:, : self.hidden] if self.attention is None else self.attention.layer(l, self.qkv_out)
+
+    def layer_step_streamed(self, L: Layer, keep=None, l: int = 0):
         M = self.M
         rms, rot = tern.TERN_QUANT_RMSNORM, tern.TERN_QUANT_FWHT128
         if keep is not None:
@@ -131,8 +203,10 @@ class DecodeModel:
         tern.tern_gemv_streamed(L.wqkv, self.x, self.qkv_out, self.ws, qflags=rms, M=M)
         if keep is not None:
             keep.append(("o_in", self.qkv_out.clone(), self.x.clone()))
-        tern.tern_gemv_streamed(L.wo, self.qkv_out[:, : self.hidden], self.x, self.ws, qflags=rms,
-                                residual=self.x, M=M)
+        o_in = self.attend(l)
+        if keep is not None and self.attention is not None:
+            keep.append(("attention", o_in.clone()))
+        tern.tern_gemv_streamed(L.wo, o_in, self.x, self.ws, qflags=rms, residual=self.x, M=M)
         if keep is not None:
             keep.append(("ffn_in", self.x.clone()))
         tern.tern_gateup_swiglu_streamed(L.wg, L.wu, self.x, self.h, self.ws, qflags=rms | rot, M=M)
@@ -140,7 +214,7 @@ class DecodeModel:
             keep.append(("down_in", self.h.clone(), self.x.clone()))
         tern.tern_gemv_streamed(L.wd, self.h, self.x, self.ws, qflags=rms, residual=self.x, M=M)
 
-    def layer_step_fused(self, L: Layer, keep=None):
+    def layer_step_fused(self, L: Layer, keep=None, l: int = 0):
         M = self.M
         rms, rot = tern.TERN_QUANT_RMSNORM, tern.TERN_QUANT_FWHT128
         if keep is not None:
@@ -149,8 +223,13 @@ class DecodeModel:
                              y_stats=self.st_qkv, M=M)
         if keep is not None:
             keep.append(("o_in", self.qkv_out.clone(), self.x.clone()))
-        tern.tern_gemv_fused(L.wo, self.qkv_out[:, : self.hidden], self.st_qkv, self.x, qflags=rms,
-                             residual=self.x, y_stats=self.st_x1, M=M)
+        o_in, o_stats = self.attend(l), self.st_qkv
+        if self.attention is not None:
+            o_stats = self.st_attn
+            tern.tern_act_stats(o_in, o_stats)
+        if keep is not None and self.attention is not None:
+            keep.append(("attention", o_in.clone()))
+        tern.tern_gemv_fused(L.wo, o_in, o_stats, self.x, qflags=rms, residual=self.x, y_stats=self.st_x1, M=M)
         if keep is not None:
             keep.append(("ffn_in", self.x.clone()))
         tern.tern_gateup_swiglu_fused(L.wg, L.wu, self.x, self.st_x1, self.h, qflags=rms | rot,
@@ -160,12 +239,15 @@ class DecodeModel:
         tern.tern_gemv_fused(L.wd, self.h, self.st_h, self.x, qflags=rms, residual=self.x,
                              y_stats=self.st_x, M=M)
 
-    def layer_step(self, L: Layer, keep=None):
+    def layer_step(self, L: Layer, keep=None, l: int = 0):
         M = self.M
         norm = tern.TERN_QUANT_RMSNORM
         tern.act_quant_fwht(self.x, self.q_h, self.s[0], 0, flags=norm)
         tern.tern_gemv(L.wqkv, self.q_h, self.s[0], self.qkv_out, M=M)
-        tern.act_quant_fwht(self.qkv_out, self.q_h, self.s[1], 0, K=self.hidden, flags=norm)
+        o_in = self.qkv_out if self.attention is None else self.attend(l)
+        if keep is not None and self.attention is not None:
+            keep.append(("attention", self.qkv_out.clone(), o_in.clone()))
+        tern.act_quant_fwht(o_in, self.q_h, self.s[1], 0, K=self.hidden, flags=norm)
         if keep is not None:
             keep.append(("o_in", self.q_h.clone(), self.s[1].clone(), self.x.clone()))
         tern.tern_gemv(L.wo, self.q_h, self.s[1], self.x, residual=self.x, M=M)
@@ -179,19 +261,18 @@ class DecodeModel:
         tern.tern_gemv(L.wd, self.q_f, self.s[3], self.x, residual=self.x, M=M)
 
     def step(self, keep=None):
-        if self.mode == "streamed":
-            for L in self.layers:
-                self.layer_step_streamed(L, keep)
-        elif self.mode == "fused":
+        if self.attention is not None:
+            self.attention.advance()
+        if self.mode == "fused":
             tern.tern_act_stats(self.x, self.st_x)
-            for L in self.layers:
-                self.layer_step_fused(L, keep)
-        else:
-            for L in self.layers:
-                self.layer_step(L, keep)
+        layer_step = {"streamed": self.layer_step_streamed, "fused": self.layer_step_fused,
+                      "unfused": self.layer_step}[self.mode]
+        for l, L in enumerate(self.layers):
+            layer_step(L, keep, l)
 
     def capture(self) -> torch.cuda.CUDAGraph:
-        """One CUDA graph holding the whole step."""
+        """One CUDA graph holding the whole step (the warming step here counts as one: with paged
+        attention set the lengths after it)."""
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
