@@ -23,8 +23,7 @@ LIBS = {
                    "csrc/tern_gemv.cu", "csrc/tern_gemv_tc.cu", "csrc/tern_gemv_stream.cu",
                    "csrc/tern_noalloc.cu", "csrc/tern_gemm.cu", "csrc/tern_tcdebug.cu",
                    "csrc/tern_debug.cu", "csrc/tern_ternarize.cu", "csrc/tern_attention.cu",
-                   "csrc/tern_paged.cu", "csrc/tern_paged_attention.cu",
-                   "csrc/tern_paged_attention_tc.cu"],
+                   "csrc/tern_paged.cu", "csrc/tern_paged_attention.cu"],
     "libtern_synth.so": ["synth_csrc/tern_synth.cu"],
 }
 HEADERS = ["csrc/tern_common.cuh", "csrc/tern_internal.h", "csrc/tern_tc.cuh",

@@ -351,7 +351,7 @@ tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_ca
     int sms = 0;
     cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) return cuda_status(e, name);
-    *bytes = tern::attention_paged_workspace_bytes(Hq, cache->Hkv, sms);
+    *bytes = tern::attention_paged_workspace_bytes(sms);
     return TERN_OK;
 }
 
@@ -373,7 +373,7 @@ tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const 
     int sms = 0;
     cudaError_t e = device_sms(&sms);
     if (e != cudaSuccess) return cuda_status(e, name);
-    if (ws_bytes < tern::attention_paged_workspace_bytes(Hq, cache->Hkv, sms))
+    if (ws_bytes < tern::attention_paged_workspace_bytes(sms))
         return fail(TERN_EINVAL, "%s: workspace too small", name);
     tern::PagedAttentionLaunch A = {q,     ldq, Hq,  *batch, *cache, window, sinks,
                                     scale, out, ldo, static_cast<float *>(workspace), sms};

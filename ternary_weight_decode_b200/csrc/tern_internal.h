@@ -132,7 +132,7 @@ struct PagedAttentionLaunch {
     float *workspace;
     int num_sms;
 };
-size_t attention_paged_workspace_bytes(int Hq, int Hkv, int num_sms);
+size_t attention_paged_workspace_bytes(int num_sms);
 cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s, const char **why);
 
 // ---------------------------------------------------------------- quant

@@ -1,492 +1,957 @@
-// tern_paged_attention.cu -- attention over the paged 8-bit KV cache.
+// tern_paged_attention.cu -- attention over the paged 8-bit KV cache on the
+// 5th-generation tensor cores, the codes used as they lie.
 //
 // out = sum_j softmax_j(scale q . k_j) v_j, one pass over the tokens with the
-// running maximum m and sum z of the softmax: a new maximum m' scales what was
-// summed before by 2^(m - m') (scores are held times log2 e).
+// running maximum m and sum z of the softmax.  Both products are matrix
+// products of the 8-bit codes with an fp32 operand written as 8-bit digits, so
+// no code is ever converted:
+//   S^T[token][row] = K[token][d] . Q[row][d]^T
+//   O^T[d][row]     = V[token][d]^T . P[token][row]
+// with 128 tokens (of S) and 128 dimensions (of O) as the 128 accumulator
+// lanes.  K is the A operand as TMA brings it (tokens x 128 bytes, K-major,
+// 128-byte swizzle), V the same bytes read the other way (M-major).
+// int8 codes (tcgen05.mma kind::i8, exact int32 sums):
+//  * A query row is scaled by a power of two to 23 bits and split into three
+//    signed 8-bit digits, q = d2 2^16 + d1 2^8 + d0 (error at most 2^-24 of the
+//    row's largest element): three columns of the B operand per row.  A digit's
+//    product is an exact int32 below 2^21.
+//  * A softmax weight times its block's value scale, relative to a reference of
+//    each, is an unsigned 32-bit fixed-point number, and its four bytes are
+//    four unsigned digits: the word is stored as it is, four columns per row.
+//    The sums over tokens are exact int32, so they stay in tensor memory from
+//    tile to tile.
+// e4m3 codes (kind::f8f6f4, fp32 sums):
+//  * A query row is scaled below 2^8 and each element written as five e4m3
+//    digits, x = d0 + (d1 + (d2 + ...) / 16) / 16, each the nearest to what is
+//    left: a digit is off by 2^-4 of it, so the five by 2^-20 of the element.
+//  * A softmax weight times its block's value scale, below 2^8 (2^2 for a new
+//    reference's largest score), likewise: off by 2^-20 of itself or, where the
+//    digits' subnormals begin, 2^-26.
+//    The fp32 sums stay in tensor memory for at most 16 tiles.
+//  A weight of 0 does not undo a NaN code: value rows that some query row does
+//  not see (the rest of a block may hold anything) lose theirs in shared memory.
+// References: row r's weights are 2^(score - m_r) with m_r at least the largest
+// score so far; when a tile has a larger one (or block scales leave the
+// reference's range, or a chain of sums ends), the sums are read, added to fp32
+// registers and begun again.  m_r is set six above the largest score, so that
+// happens a few times per item (26 of int8's 32 bits remain; block scales may
+// cost 8 more).
 //
-// attn_split_paged_kernel.  The rows of one sequence that share a KV head (its
-// tokens times the query heads of the group) are taken eight at a time: an
-// item.  An item's work is its visible tiles of 16 tokens (one scale block
-// each).  All tiles of all items form one line, cut into equal ranges, one per
-// warp of the grid, so that uneven contexts fill the GPU evenly; the lengths
-// are read on the device.  A warp walks its range without waiting for others:
-// the ring of TMA stages runs on across items.  An item that lies inside one
-// warp's range is written out by it; the pieces of the others (m, z and the
-// unnormalised sum) are merged in the order of the ranges, first those of a
-// CTA through shared memory, then those of several CTAs through the workspace,
-// by the CTA that finishes the last of them, so the result does not depend on
-// timing.
-//
-// TMA brings the 16 key and 16 value rows of a tile (2 KB each, 128-byte
-// swizzle) into the warp's own stages, and the warp multiplies on the tensor
-// cores with fp16 operands and fp32 accumulators (m16n8k16).  Codes of 8 bits
-// are exact in fp16.  Queries and softmax weights are fp32 values, held as two
-// fp16 parts hi + lo (22 bits, the query row first scaled by a power of two):
-// the eight rows' hi parts fill rows 0-7 of the 16-row operand and their lo
-// parts rows 8-15, so the second part costs no further matrix instruction, and
-// the two halves of a result lie in one thread.  The value product of each
-// tile starts from zero and is added to the fp32 sum with the block's scale,
-// so that no long chain of sums runs inside the tensor cores.
-//
-// The order of the 128 dimensions inside a score's sum is free: lane (g, t)
-// (g = lane / 4, t = lane % 4) feeds bytes 32t .. 32t+31 of key g, two 16-byte
-// loads; likewise output column n of value product i is dimension 16 n + i, so
-// a lane's value operands are 16 contiguous bytes of four tokens.
+// One CTA per SM.  Warps of their own copy K and V, issue QK, issue PV and
+// make the query digits (issuing takes a thread some 450 cycles a product; one
+// warp for both took longer than a tile's bytes).  Two softmax groups (thread =
+// token of S, dimension of O; with 32 rows each group is two warpgroups of 16)
+// take the tiles in turn, each with its own accumulators, references and weight
+// buffer, so that one group's waits, fences and barriers pass under the other's
+// arithmetic; what they have of an item is put together at its end.  A tile is
+// eight visible blocks of 16 tokens of an item, from anywhere in the sequence,
+// so sinks and a window fill whole tiles.  Everything runs ahead across items:
+// K and V by rings of their own (a K stage is free after QK, a V stage after
+// PV), QK of the next tiles before PV of this one, the next item's digits while
+// this one's tiles are worked off.
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include <algorithm>
 
 #include "tern_paged_attention.cuh"
+#include "tern_tc.cuh"
 
 namespace tern {
 
 namespace {
 
-constexpr int kWarps = 12;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 8;         // rows of an item
-constexpr int kStages = 3;       // tiles in flight per warp
-constexpr int kBatch = 16;       // tiles whose places are looked up at a time, one a lane
-constexpr int kTileBytes = kPB * kPD;       // 2048: one block's codes of K or of V
-constexpr int kStageBytes = 2 * kTileBytes;
-constexpr float kPScale = 8.0f;  // softmax weights are held times 2^8: their lo parts stay normal in fp16
+constexpr int kTok = kTB * kPB;           // 128 tokens
+constexpr int kTileBytes = kTok * kPD;    // 16 KB of K or V codes
+constexpr int kInfo = 16;                 // tile infos kept: K's ring runs at most kStages + kSBufs + 2 tiles ahead of the softmax
+constexpr int kItems = 8;                 // items kept for the query warp, and whose score scales are kept
+constexpr float kHeadroom = 6.0f;         // a new reference lies this far (log2) above the largest score
+constexpr int kChainInt8 = 256;           // tiles summed in int32: 256 * 128 * 255 * 127 < 2^31
+constexpr int kChainE4m3 = 16;            // tiles summed in fp32 inside the tensor cores (16 or 64: the same time)
+constexpr float kVRange = 1.0f / 256.0f;  // largest block scale of a tile, relative to the reference
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The same from zero.
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-
-// Two fp32 values as fp16 pairs hi + lo.
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    const __half2 h = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(h);
-    hi = as_u32(h);
-    lo = as_u32(__floats2half2_rn(x - f.x, y - f.y));
-}
-
-// Codes c0 c1 (low half of the pair's bytes) as fp16 x 2.  int8: 1024 + (c +
-// 128) has the code's bits as its low byte (fp16 spacing 1 there), and one
-// subtraction leaves c; the caller has flipped the sign bits.  e4m3: the
-// conversion instruction.
-template <int KIND, int SEL>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-    if constexpr (KIND == TERN_KV_INT8) {
-        const uint32_t m = __byte_perm(w, 0x64646464u, SEL ? 0x4342 : 0x4140);
-        return as_u32(__hsub2(*reinterpret_cast<const __half2 *>(&m), __half2(__half(1152.0f), __half(1152.0f))));
-    } else {
-        uint32_t r;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(SEL ? w >> 16 : w & 0xFFFFu)));
-        return r;
-    }
-}
-template <int KIND>
-__device__ __forceinline__ uint32_t flip(uint32_t w) {
-    return KIND == TERN_KV_INT8 ? w ^ 0x80808080u : w;
-}
-
-// The running softmax of one warp: row g's reference (its maximum less
-// kPScale; weights are 2^(score - m)) and this lane's part of its sum, and the
-// lane's output columns (dimensions 32 t + i and 32 t + 16 + i).
-struct State {
-    float m, z;
-    float2 o[16];
+template <int R, int KIND>
+struct Shape {
+    static constexpr bool kInt = KIND == TERN_KV_INT8;
+    static constexpr int kHalves = R == 32 ? 2 : 1;   // warpgroups of a softmax group
+    static constexpr int kRW = R / kHalves;           // rows of each
+    static constexpr int kHelpers = R == 32 ? 4 : 8;  // warps in front of the softmax warps
+    static constexpr int kThreads = 32 * kHelpers + 2 * kHalves * 128;
+    static constexpr int kGroup = 128 * kHalves;      // threads of a softmax group
+    // warps: copies of K (of K and V with 4 helpers), of V, issue of QK, of PV, query digits
+    static constexpr int kWarpK = 0, kWarpV = kHelpers == 8 ? 1 : -1, kWarpQK = kHelpers == 8 ? 2 : 1,
+                         kWarpPV = kHelpers == 8 ? 3 : 2, kWarpQ = kHelpers == 8 ? 4 : 3;
+    static constexpr int kSBufs = R == 32 ? 2 : 4;    // S accumulators
+    static constexpr int kQD = kInt ? 3 : 5;          // digits of a query, columns of S per row
+    static constexpr int kVD = kInt ? 4 : 5;         // digits of a weight, columns of O per row
+    static constexpr int kNS = (kQD * R + 15) / 16 * 16;
+    static constexpr int kNP = (kVD * R + 15) / 16 * 16;
+    static constexpr int kPRow = kNP == 32 ? 32 : 128;  // bytes of a token's row of weight digits
+    static constexpr int kStages = R == 32 ? 3 : kInt && R == 8 ? 6 : 5;    // of K
+    static constexpr int kVStages = R == 32 || R == 16 ? 4 : kInt ? 6 : 5;  // of V (held longer: until PV)
+    static constexpr int kQBytes = kNS * 128;
+    static constexpr int kPBytes = kTok * kPRow;      // (also holds a group's own R x 128 sums at the end of an item)
+    static constexpr int kSumBytes = R * kPD * 4;     // the sums that one group hands to the other
+    static constexpr uint32_t kO = kSBufs * kNS;      // first column of O
+    static constexpr uint32_t kTmemCols = kSBufs * kNS + 2 * kNP <= 256 ? 256 : 512;
+    static_assert(kSBufs * kNS + 2 * kNP <= kTmemCols && kSumBytes <= kPBytes, "tensor memory; sums in the weight buffer");
+    static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "operand tiles begin on 1024 bytes");
 };
 
-// What a warp's walk needs of one tile.
-struct __align__(16) TileInfo {
-    int bi;          // scale block of K and V (its 16 rows begin at 16 bi), -1: none
-    float ks, vs;
-    int j0;          // first token
-    int b, head, rt; // item
-    int k;           // tile of the item, times 2, + 1 for the item's last tile
-};
-
-// A warp's piece of an item that others share.
-struct Piece {
-    int valid, ends;   // ends: holds the item's last tile
-    int head, rt, units;
+// One tile, as the softmax and MMA warps see it.
+struct TileInfo {
+    float ks[kTB], vs[kTB];
+    int j0[kTB];      // first token of each block
+    int row[kTB];     // its first code row, for the block that begins a copy
+    int size[kTB];    // log2 of the blocks that this copy takes, -1: none begins here
+    int valid;        // bit j: block j is there
+    int flags;
+    float vmax;       // largest value scale
+    int head, rt, k, units, ord;
     Seq s;
-    long long u0;      // line index of the item's first tile
+};
+// An item, as the query warp sees it.
+struct ItemInfo {
+    int head, rt;
+    int tiles;        // of this CTA
+    Seq s;
+};
+enum : int {
+    kFirst = 1,       // the first tile of its item in this CTA
+    kLast = 2,        // the last
+    kGroupFirst = 4,  // the first of its item that its group has here
+    kGroupLast = 8,   // the last
+    kBoth = 16,       // both groups have tiles of the item
+    kEdge = 32,       // masks needed
+    kEnds = 64,       // the item's last tile
 };
 
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kPieceFloats = kRows * kPD;
-struct SplitShared {
-    float first[kWarps][kPieceFloats];  // the piece a warp's range begins with (its last piece lies in its ring)
-    TileInfo info[kWarps][2][kBatch];
-    float m[kWarps][2][kRows], z[kWarps][2][kRows];
-    Piece piece[kWarps][2];
-    uint64_t bars[kWarps][kStages];
+template <int R, int KIND>
+struct AttnShared {
+    using Sh = Shape<R, KIND>;
+    TileInfo info[kInfo];
+    ItemInfo item[kItems], first_item;
+    float4 rowf[kItems][R / 4];        // score scale of each row's digits
+    float4 m[2][R / 4], mref[2][R / 4];  // each group's references; mref: 0 for a row that has seen nothing
+    float4 back[2][R / 4];            // what new references make of the sums before
+    float wmax[2][4][R];
+    float zsum[2][4][R];
+    float sum_m[R], sum_z[R];         // references and sums of the part of an item that a group hands to the other
+    float2 factors[2][R];             // of the parts at an item's end
     LineShared line;
+    uint64_t k_full[Sh::kStages], k_empty[Sh::kStages], v_full[Sh::kVStages], v_empty[Sh::kVStages];
+    uint64_t info_full[kInfo], item_full[kItems], item_empty[kItems];
+    uint64_t s_full[Sh::kSBufs], s_empty[Sh::kSBufs], p_full[2], p_empty[2], q_full[2], q_empty[2], sum_full, sum_empty;
     CutItem cut[2];
+    uint32_t tmem;
+    int accumulate[2];
     int last[2];
 };
-constexpr size_t kSplitSmem = kRingBytes + sizeof(SplitShared) + 1024;
-static_assert(kSplitSmem <= 227 * 1024, "shared memory of one CTA");
 
-template <int KIND>
-__global__ void __launch_bounds__(kThreads, 1)
-    attn_split_paged_kernel(AttnParams p, const __grid_constant__ CUtensorMap kmap,
-                            const __grid_constant__ CUtensorMap vmap) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    SplitShared &S = *reinterpret_cast<SplitShared *>(ring + kRingBytes);
+template <int R, int KIND>
+constexpr size_t attn_smem() {
+    using Sh = Shape<R, KIND>;
+    return (Sh::kStages + Sh::kVStages) * kTileBytes + 2 * Sh::kPBytes + 2 * Sh::kQBytes + Sh::kSumBytes +
+           sizeof(AttnShared<R, KIND>) + 1024;
+}
+static_assert(attn_smem<8, TERN_KV_INT8>() <= 227 * 1024 && attn_smem<16, TERN_KV_INT8>() <= 227 * 1024 &&
+                  attn_smem<32, TERN_KV_INT8>() <= 227 * 1024 &&
+                  attn_smem<8, TERN_KV_E4M3>() <= 227 * 1024 && attn_smem<16, TERN_KV_E4M3>() <= 227 * 1024,
+              "shared memory of one CTA");
+
+// B operand descriptor of the weight digits, N-major: a token's row of ROW
+// bytes, 128 (128-byte swizzle, layout 2) or 32 (32-byte swizzle, layout 6:
+// 16-byte chunk c of row k stored at c ^ (k / 4 % 2)), groups of 8 tokens 8 rows apart.
+template <int ROW>
+__device__ __forceinline__ uint64_t weights_desc(uint32_t saddr) {
+    if constexpr (ROW == 32)
+        return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (static_cast<uint64_t>(256u >> 4) << 32) |
+               (1ull << 46) | (6ull << 61);
+    return smem_desc_sw128(saddr);
+}
+template <int ROW>
+__device__ __forceinline__ int weights_chunk(int c, int k) {
+    return ROW == 32 ? c ^ (k >> 2 & 1) : c ^ (k & 7);
+}
+
+// Two values as their next e4m3 digits (two bytes), and what is left of them,
+// times 16 (|x| <= 256; a digit is off by at most 2^-4 of the value).
+__device__ __forceinline__ uint32_t e4m3_digit(float2 &x) {
+    const __nv_fp8x2_storage_t d = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(d, __NV_E4M3)));
+    x = __fmul2_rn(__fadd2_rn(x, make_float2(-f.x, -f.y)), make_float2(16.0f, 16.0f));
+    return d;
+}
+
+// A wait of this thread; once one has run out, none of the later ones waits.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
+    if (ok && !mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity);
+}
+
+// An int32 of at most 22 bits as fp32, exactly, without the conversion unit.
+__device__ __forceinline__ float small_int(uint32_t c) {
+    return __uint_as_float(c + 0x4B400000u) - 12582912.0f;
+}
+
+__device__ __forceinline__ uint32_t to_u32_sat(float x) {
+    uint32_t u;
+    asm("cvt.rni.u32.f32 %0, %1;" : "=r"(u) : "f"(x));
+    return u;
+}
+
+__device__ __forceinline__ float redux_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Barrier over the N threads of softmax group g, with the "or" of x.
+template <int N>
+__device__ __forceinline__ bool any_of(bool x, int g) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x)), "r"(1 + g), "n"(N)
+        : "memory");
+    return r != 0;
+}
+
+// Sums of each z[r] over the warp; lane l ends up with that of row l % R.
+template <int R>
+__device__ __forceinline__ float sum_rows(float (&z)[R], int lane) {
+#pragma unroll
+    for (int h = R / 2; h >= 1; h >>= 1) {
+        const bool up = (lane & h) != 0;
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? z[j] : z[j + h], h);
+            z[j] = (up ? z[j + h] : z[j]) + other;
+        }
+    }
+#pragma unroll
+    for (int h = R; h < 32; h <<= 1) z[0] += __shfl_xor_sync(0xffffffffu, z[0], h);
+    return z[0];
+}
+
+// Adds what PV has summed to o, times the value reference: of int8, four digit
+// columns a row, of value 2^(8 k - 32); of e4m3, R columns a digit, of value
+// 2^(-8 - 4 k).
+template <int R, int KIND>
+__device__ __forceinline__ void add_sums(uint32_t taddr, float vref, float (&o)[Shape<R, KIND>::kRW]) {
+    constexpr int RW = Shape<R, KIND>::kRW;
+    if constexpr (KIND == TERN_KV_INT8) {
+#pragma unroll
+        for (int h = 0; h < RW / 8; ++h) {
+            uint32_t ov[32];
+            tmem_ld32(taddr + 32 * h, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float t = static_cast<float>(static_cast<int>(ov[4 * e])) * 0x1p-32f;
+                t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 1])), 0x1p-24f, t);
+                t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 2])), 0x1p-16f, t);
+                t = fmaf(static_cast<float>(static_cast<int>(ov[4 * e + 3])), 0x1p-8f, t);
+                o[8 * h + e] = fmaf(t, vref, o[8 * h + e]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < RW / 8; ++h) {
+            uint32_t ov[5][8];
+#pragma unroll
+            for (int k = 0; k < 5; ++k) tmem_ld8(taddr + R * k + 8 * h, ov[k]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float t = 0.0f;
+#pragma unroll
+                for (int k = 4; k >= 0; --k) t = fmaf(t, 0.0625f, __uint_as_float(ov[k][e]));
+                o[8 * h + e] = fmaf(t, vref * 0x1p-8f, o[8 * h + e]);
+            }
+        }
+    }
+}
+
+// Look-up of a range's tiles, and K's copies (with COPY_V, V's too): writes the
+// infos of the items and tiles.
+template <int R, int KIND, bool COPY_V, typename SeqOf>
+__device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *kring,
+                                          uint8_t *vring, const Line &L, const Ranges &ranges, long long u0, int count,
+                                          SeqOf seq_of) {
+    constexpr int kSt = Shape<R, KIND>::kStages, kVSt = Shape<R, KIND>::kVStages;
     const PagedView &v = p.v;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int c = blockIdx.x;
-    uint8_t *my_ring = ring + warp * kStages * kStageBytes;
-
-    if (tid == 0) {
-        prefetch_tmap(&kmap);
-        prefetch_tmap(&vmap);
-    }
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(&S.bars[warp][s], 1);
-        fence_mbar_init();
-        S.piece[warp][0].valid = S.piece[warp][1].valid = 0;
-        S.piece[warp][0].ends = 0;
-        if (warp < 2) S.cut[warp].valid = 0;
-    }
-    pdl_wait();
-
-    // ---- the line of tiles, and this warp's range of it
-    const Line L = make_line<kRows, 1>(p, S.line);
-    const long long total = L.total;
-    auto seq_of = [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); };
-    const int nw = static_cast<int>(min(static_cast<long long>(gridDim.x) * kWarps, total));
-    Ranges R = {0, 0};
-    if (total > 0) {
-        R.base = quot(total, nw);
-        R.more = total - R.base * nw;
-    }
-    const int wi = c * kWarps + warp;  // this warp's range
-    const long long u0 = wi < nw ? R.begin(wi) : 0;
-    const int count = wi < nw ? static_cast<int>(R.begin(wi + 1) - u0) : 0;
-
-    if (count > 0) {
-        Cursor<1> cur = find_place<kRows, 1>(p, S.line, L, u0, seq_of);
-        // lane l < kBatch keeps the cursor of tiles l, l + kBatch, ...: tile i of the range is in
-        // info[i / kBatch % 2][i % kBatch]
-        auto info = [&](int i) -> TileInfo & { return S.info[warp][(i / kBatch) & 1][i % kBatch]; };
-        int step = lane;
-        auto fill = [&](int i0) {
-            if (lane < kBatch && i0 + lane < count) {
-                advance<kRows>(p, cur, step, seq_of);
-                step = kBatch;
-                TileInfo x;
-                x.j0 = cur.tl.block(cur.k) * kPB;
-                x.b = cur.b;
-                x.head = cur.head;
-                x.rt = cur.rt;
-                x.k = 2 * cur.k + (cur.k + 1 == cur.units() ? 1 : 0);
-                x.bi = -1;
-                x.ks = x.vs = 0.0f;
-                if (cur.tl.n > 0) {
-                    const int64_t bi = block_index(v, cur.b, cur.tl.block(cur.k));
-                    if (bi >= 0) {
-                        x.bi = static_cast<int>(bi) + cur.head * v.bpp;
-                        x.ks = v.ks[x.bi];
-                        x.vs = v.vs[x.bi];
-                    }
+    const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
+    bool ok = true;
+    // four tiles at a time (lane = 8 * tile + block): a batch is looked up while the one before is copied
+    Cursor cur = find_place<R>(p, S.line, L, u0, seq_of);
+    const int k_first = cur.k;
+    if (lane == 0) S.first_item = {cur.head, cur.rt, cur.units(), cur.s};
+    int step = sub, bi = -1, j0 = 0;
+    float ks = 0.0f, vs = 0.0f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < count + 4; i0 += 4) {
+        const int b_now = bi, j0_now = j0;
+        const float ks_now = ks, vs_now = vs;
+        const Cursor it = cur;
+        bi = -1;
+        ks = vs = 0.0f;
+        if (i0 + sub < count) {  // this lane's block of tile i0 + sub
+            advance<R>(p, cur, step, seq_of);
+            step = 4;
+            if (j == 0 && (cur.k == 0 || i0 + sub == 0)) {
+                const int slot = cur.ord % kItems;
+                wait(&S.item_empty[slot], ((cur.ord / kItems) + 1) & 1, ok);
+                S.item[slot].head = cur.head;
+                S.item[slot].rt = cur.rt;
+                S.item[slot].tiles = min(cur.units() - cur.k, count - i0 - sub);
+                S.item[slot].s = cur.s;
+                mbar_arrive(&S.item_full[slot]);
+            }
+            const int kb = kTB * cur.k + j;
+            if (kb < cur.tl.n) {
+                const int blk = cur.tl.block(kb);
+                j0 = blk * kPB;
+                const int64_t x = block_index(v, cur.b, blk);
+                if (x >= 0) {
+                    bi = static_cast<int>(x) + cur.head * v.bpp;
+                    ks = v.ks[bi];
+                    vs = v.vs[bi];
                 }
-                info(i0 + lane) = x;
+            }
+        }
+        __syncwarp();
+        if (i0 == 0) continue;
+        const unsigned there = __ballot_sync(0xffffffffu, b_now >= 0);
+        // runs of blocks that lie behind one another in the cache: one copy each for 8, 4, 2 or 1 of them
+        // (copies of 16 rows: 2150 cycles a tile, of 64 rows 1690)
+        const int before = __shfl_up_sync(0xffffffffu, b_now, 1);
+        const unsigned follows = __ballot_sync(0xffffffffu, b_now >= 0 && b_now == before + 1) >> (8 * sub);
+        int size = 0;  // log2 of the blocks this lane copies, -1: another lane does
+        if ((follows & 0xFEu) == 0xFEu) size = 3;
+        else if ((follows >> (j & 4) & 0xEu) == 0xEu) size = 2;
+        else if (follows >> (j & 6) & 2u) size = 1;
+        if (b_now < 0 || (j & ((1 << size) - 1))) size = -1;
+        // masks: a block whose tokens not every row sees, or that is missing
+        const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
+        const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
+        const bool whole = b_now >= 0 && j0_now + kPB - 1 <= p_min &&
+                           (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
+        const unsigned not_whole = __ballot_sync(0xffffffffu, !whole);
+        float vmax = vs_now;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+#pragma unroll 1
+        for (int e = 0; e < 4 && i0 - 4 + e < count; ++e) {
+            const int i = i0 - 4 + e, stage = i % kSt;
+            wait(&S.k_empty[stage], ((i / kSt) + 1) & 1, ok);
+            if (sub == e) {
+                TileInfo &f = S.info[i % kInfo];
+                f.ks[j] = ks_now;
+                f.vs[j] = vs_now;
+                f.j0[j] = j0_now;
+                f.row[j] = b_now * kPB;
+                f.size[j] = size;
+                if (j == 0) {
+                    const int since = min(it.k, i), left = min(it.units() - 1 - it.k, count - 1 - i);
+                    f.valid = there >> (8 * e) & 255;
+                    f.flags = (since == 0 ? kFirst : 0) | (left == 0 ? kLast : 0) | (since < 2 ? kGroupFirst : 0) |
+                              (left < 2 ? kGroupLast : 0) | (since + left > 0 ? kBoth : 0) |
+                              ((not_whole >> (8 * e) & 255) ? kEdge : 0) | (it.k + 1 == it.units() ? kEnds : 0);
+                    f.vmax = vmax;
+                    f.head = it.head;
+                    f.rt = it.rt;
+                    f.k = it.k;
+                    f.units = it.units();
+                    f.ord = it.ord;
+                    f.s = it.s;
+                }
+            }
+            const uint32_t bytes = __popc(there >> (8 * e) & 255) * kPB * kPD;
+            const int at = j * kPB * kPD;
+            __syncwarp();
+            if (lane == 8 * e) {
+                mbar_arrive_expect_tx(&S.k_full[stage], bytes);
+                mbar_arrive(&S.info_full[i % kInfo]);
             }
             __syncwarp();
-        };
-        auto start = [&](int i) {  // tile i's copies into its stage
-            if (lane == 0 && i < count) {
-                const int bi = info(i).bi;
-                if (bi >= 0) {
-                    uint8_t *dst = my_ring + (i % kStages) * kStageBytes;
-                    uint64_t *bar = &S.bars[warp][i % kStages];
-                    mbar_arrive_expect_tx(bar, kStageBytes);
-                    tma_load_2d_nohint(dst, &kmap, 0, bi * kPB, bar);
-                    tma_load_2d_nohint(dst + kTileBytes, &vmap, 0, bi * kPB, bar);
-                }
-            }
-        };
-
-        State st;
-        uint32_t qhi[8][2], qlo[8][2];
-        Seq s = {};
-        float rowf = 0.0f;
-        int pos = 0, p_min = 0, p_max = 0, k_first = 0;
-        uint32_t phases = 0;  // parity of each stage
-        int stage = 0;
-#pragma unroll 1
-        for (int i = -1; i < count; ++i) {
-            // look up the first batch, and the batch behind the next while this one is worked off
-            if (i < 0 || (i % kBatch == 0 && i + kBatch < count)) fill(i < 0 ? 0 : i + kBatch);
-            if (i < 0) {
-#pragma unroll 1
-                for (int e = 0; e < kStages; ++e) start(e);
-                continue;
-            }
-            const TileInfo x = info(i);
-            if (i == 0 || (x.k >> 1) == 0) {
-                // ---- a new item: row g's query, dimensions 32 t .. 32 t + 31, as hi + lo operands
-                s = seq_of(x.b);
-                k_first = x.k >> 1;
-                const int r = kRows * x.rt + g;
-                const bool row_ok = r < s.rows;
-                const int ri = row_ok ? p.by_gq.quot(r) : 0;
-                pos = s.first + ri;
-                p_min = s.first + p.by_gq.quot(kRows * x.rt);
-                p_max = s.first + p.by_gq.quot(min(kRows * x.rt + kRows, s.rows) - 1);
-                const float *qp = p.q + static_cast<int64_t>(s.start + ri) * p.ldq +
-                                  (x.head * p.GQ + (row_ok ? r : 0) - ri * p.GQ) * kPD + 32 * t;
-                float4 q4[8];
-                float amax = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    q4[e] = row_ok ? *reinterpret_cast<const float4 *>(qp + 4 * e) : make_float4(0, 0, 0, 0);
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(q4[e].x), fabsf(q4[e].y)), fmaxf(fabsf(q4[e].z), fabsf(q4[e].w))));
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // the row times 2^e: its largest value in [2^7, 2^8)
-                const int e = max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23)));
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                rowf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    split2(q4[n].x * up, q4[n].y * up, qhi[n][0], qlo[n][0]);
-                    split2(q4[n].z * up, q4[n].w * up, qhi[n][1], qlo[n][1]);
-                }
-                st.m = -INFINITY;
-                st.z = 0.0f;
-#pragma unroll
-                for (int n = 0; n < 16; ++n) st.o[n] = make_float2(0.0f, 0.0f);
-            }
-            if (x.bi >= 0) {
-                mbar_wait_bounded(&S.bars[warp][stage], (phases >> stage) & 1u);
-                phases ^= 1u << stage;
-                const uint8_t *kt = my_ring + stage * kStageBytes, *vt = kt + kTileBytes;
-                // scores: tokens j0 + 2t, + 1 (n = 0) and j0 + 8 + 2t, + 1 (n = 1) of row g
-                float sc[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[n][e] = 0.0f;
-                    const uint8_t *row = kt + (8 * n + g) * kPD;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 w4 = lds128(row + (((2 * t + h) ^ g) << 4));
-                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i8 = 4 * h + e;
-                            const uint32_t f = flip<KIND>(w[e]);
-                            const uint32_t a[4] = {qhi[i8][0], qlo[i8][0], qhi[i8][1], qlo[i8][1]};
-                            mma_f16(sc[n], a, code_pair<KIND, 0>(f), code_pair<KIND, 1>(f));
-                        }
-                    }
-                }
-                const float f = rowf * x.ks;
-                float y[4] = {(sc[0][0] + sc[0][2]) * f, (sc[0][1] + sc[0][3]) * f, (sc[1][0] + sc[1][2]) * f,
-                              (sc[1][1] + sc[1][3]) * f};
-                const bool whole = x.j0 + kPB - 1 <= p_min &&
-                                   (p.window == 0 || x.j0 > p_max - p.window || x.j0 + kPB <= p.sinks);
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = x.j0 + (e >> 1) * 8 + 2 * t + (e & 1);
-                        if (j > pos || (p.window > 0 && j <= pos - p.window && j >= p.sinks)) y[e] = -INFINITY;
-                    }
-                }
-                float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(st.m, mx - kPScale);
-                const float ref = mn == -INFINITY ? 0.0f : mn;
-                if (__any_sync(0xffffffffu, mn != st.m)) {
-                    const float corr = ex2(st.m - ref);  // 0 when nothing was seen before
-                    st.z *= corr;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) st.o[k] = __fmul2_rn(st.o[k], make_float2(corr, corr));
-                    st.m = mn;
-                }
-                float w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = ex2(y[e] - ref);
-                st.z += (w[0] + w[1]) + (w[2] + w[3]);
-                uint32_t a[4];
-                split2(w[0], w[1], a[0], a[1]);
-                split2(w[2], w[3], a[2], a[3]);
-                // values: tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile, dimensions 16 g .. 16 g + 15
-                uint32_t vw[4][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int rr = 2 * t + (k & 1) + 8 * (k >> 1);
-                    const uint4 w4 = lds128(vt + rr * kPD + ((g ^ (rr & 7)) << 4));
-                    vw[k][0] = w4.x;
-                    vw[k][1] = w4.y;
-                    vw[k][2] = w4.z;
-                    vw[k][3] = w4.w;
-                    if (x.j0 + kPB > s.end && x.j0 + rr >= s.end)  // slots behind the context hold anything
-                        vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0;
-                }
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const uint32_t x0 = flip<KIND>(vw[0][q4]), x1 = flip<KIND>(vw[1][q4]);
-                    const uint32_t y0 = flip<KIND>(vw[2][q4]), y1 = flip<KIND>(vw[3][q4]);
-                    const uint32_t xl = __byte_perm(x0, x1, 0x5140), xh = __byte_perm(x0, x1, 0x7362);
-                    const uint32_t yl = __byte_perm(y0, y1, 0x5140), yh = __byte_perm(y0, y1, 0x7362);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float d[4];
-                        if (e == 0) mma_f16_zero(d, a, code_pair<KIND, 0>(xl), code_pair<KIND, 0>(yl));
-                        if (e == 1) mma_f16_zero(d, a, code_pair<KIND, 1>(xl), code_pair<KIND, 1>(yl));
-                        if (e == 2) mma_f16_zero(d, a, code_pair<KIND, 0>(xh), code_pair<KIND, 0>(yh));
-                        if (e == 3) mma_f16_zero(d, a, code_pair<KIND, 1>(xh), code_pair<KIND, 1>(yh));
-                        const float2 sum = __fadd2_rn(make_float2(d[0], d[1]), make_float2(d[2], d[3]));
-                        st.o[4 * q4 + e] = __ffma2_rn(make_float2(x.vs, x.vs), sum, st.o[4 * q4 + e]);
-                    }
-                }
-                fence_proxy_async_smem();  // these reads before the refill of the stage
+            if (sub == e && size >= 0) tma_load_2d_nohint(kring + stage * kTileBytes + at, &maps.k[size], 0, b_now * kPB, &S.k_full[stage]);
+            if (COPY_V) {
+                const int vs = i % kVSt;
+                wait(&S.v_empty[vs], ((i / kVSt) + 1) & 1, ok);
+                if (lane == 8 * e) mbar_arrive_expect_tx(&S.v_full[vs], bytes);
                 __syncwarp();
+                if (sub == e && size >= 0)
+                    tma_load_2d_nohint(vring + vs * kTileBytes + at, &maps.v[size], 0, b_now * kPB, &S.v_full[vs]);
             }
-            start(i + kStages);
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+        }
+    }
+    // the items that other CTAs have parts of
+    if (lane == 0 && k_first > 0) {
+        const ItemInfo &it = S.first_item;
+        note_cut(S.cut[0], ranges, it.head, it.rt, it.s, u0 - k_first, it.tiles);
+    }
+    // (the last tile's item, as the lane that looked it up has it: cut if it goes on and began in this range)
+    if (j == 0 && sub == (count - 1) % 4 && cur.k + 1 < cur.units() && cur.k <= count - 1)
+        note_cut(S.cut[1], ranges, cur.head, cur.rt, cur.s, u0 + count - 1 - cur.k, cur.units());
+    // no copy is in flight when the CTA ends, even after a wait that ran out
+    bool land = true;
+#pragma unroll 1
+    for (int i = max(0, count - kSt); i < count; ++i) wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
+    if (COPY_V)
+#pragma unroll 1
+        for (int i = max(0, count - kVSt); i < count; ++i) wait(&S.v_full[i % kVSt], (i / kVSt) & 1, land);
+}
 
-            const bool ends = (x.k & 1) != 0;
-            if (ends || i + 1 == count) {
-                // ---- the item, or this warp's piece of it, is done
-                st.z += __shfl_xor_sync(0xffffffffu, st.z, 1);
-                st.z += __shfl_xor_sync(0xffffffffu, st.z, 2);
-                const int r = kRows * x.rt + g;
-                if (k_first == 0 && ends) {
-                    if (r < s.rows) {
+// V's copies, by the tiles' infos; lanes 0-7 a block each.
+template <int R, int KIND>
+__device__ __forceinline__ void copy_values(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *vring, int count) {
+    constexpr int kSt = Shape<R, KIND>::kVStages;
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        const int stage = i % kSt;
+        wait(&S.info_full[i % kInfo], (i / kInfo) & 1, ok);
+        const TileInfo &f = S.info[i % kInfo];
+        const int size = lane < kTB ? f.size[lane] : -1, row = lane < kTB ? f.row[lane] : 0;
+        wait(&S.v_empty[stage], ((i / kSt) + 1) & 1, ok);
+        if (lane == 0) mbar_arrive_expect_tx(&S.v_full[stage], __popc(f.valid) * kPB * kPD);
+        __syncwarp();
+        if (size >= 0)
+            tma_load_2d_nohint(vring + stage * kTileBytes + lane * kPB * kPD, &maps.v[size], 0, row, &S.v_full[stage]);
+    }
+    bool land = true;
+#pragma unroll 1
+    for (int i = max(0, count - kSt); i < count; ++i) wait(&S.v_full[i % kSt], (i / kSt) & 1, land);
+}
+
+template <int KIND>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (KIND == TERN_KV_INT8)
+        mma_i8_ss(d, a, b, idesc, accumulate);
+    else
+        mma_e4m3_ss(d, a, b, idesc, accumulate);
+}
+
+template <int R, int KIND>
+__global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
+    attn_paged_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CacheMaps maps) {
+    using Sh = Shape<R, KIND>;
+    constexpr bool kInt = Sh::kInt;
+    constexpr int kSt = Sh::kStages, kRW = Sh::kRW, kGroup = Sh::kGroup;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *kring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *vring = kring + kSt * kTileBytes;
+    uint8_t *pbuf = vring + Sh::kVStages * kTileBytes;
+    uint8_t *qbuf = pbuf + 2 * Sh::kPBytes;
+    float *handed = reinterpret_cast<float *>(qbuf + 2 * Sh::kQBytes);
+    AttnShared<R, KIND> &S = *reinterpret_cast<AttnShared<R, KIND> *>(qbuf + 2 * Sh::kQBytes + Sh::kSumBytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = blockIdx.x;
+    bool ok = true;
+
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            prefetch_tmap(&maps.k[i]);
+            prefetch_tmap(&maps.v[i]);
+        }
+        for (int i = 0; i < kSt; ++i) {
+            mbar_init(&S.k_full[i], 1);
+            mbar_init(&S.k_empty[i], 1);
+        }
+        for (int i = 0; i < Sh::kVStages; ++i) {
+            mbar_init(&S.v_full[i], 1);
+            mbar_init(&S.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.p_full[i], 4 * Sh::kHalves);
+            mbar_init(&S.p_empty[i], 1);
+            mbar_init(&S.q_full[i], 1);
+            mbar_init(&S.q_empty[i], 1);
+            S.cut[i].valid = 0;
+        }
+        mbar_init(&S.sum_full, 4 * Sh::kHalves);
+        mbar_init(&S.sum_empty, 4 * Sh::kHalves);
+        for (int i = 0; i < kInfo; ++i) mbar_init(&S.info_full[i], 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&S.item_full[i], 1);
+            mbar_init(&S.item_empty[i], 1);
+        }
+        for (int i = 0; i < Sh::kSBufs; ++i) {
+            mbar_init(&S.s_full[i], 2);
+            mbar_init(&S.s_empty[i], 4 * Sh::kHalves);
+        }
+        fence_mbar_init();
+    }
+    if (warp == Sh::kWarpQK) {
+        tmem_alloc(&S.tmem, Sh::kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    tc_fence_before_sync();
+    const Line L = make_line<R>(p, S.line);
+    tc_fence_after_sync();
+    const int G = static_cast<int>(min(static_cast<long long>(gridDim.x), L.total));
+    Ranges ranges = {0, 0};
+    if (L.total > 0) {
+        ranges.base = quot(L.total, G);
+        ranges.more = L.total - ranges.base * G;
+    }
+    const long long u0 = c < G ? ranges.begin(c) : 0;
+    const int count = c < G ? static_cast<int>(ranges.begin(c + 1) - u0) : 0;
+    const uint32_t tmem = S.tmem;
+
+    if (count == 0) {
+    } else if (warp == Sh::kWarpK) {
+        auto seq_of = [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); };
+        copy_keys<R, KIND, (Sh::kWarpV < 0)>(p, maps, S, kring, vring, L, ranges, u0, count, seq_of);
+    } else if (warp == Sh::kWarpV) {
+        copy_values<R, KIND>(maps, S, vring, count);
+    } else if (warp == Sh::kWarpQK) {
+        // ---- S of each tile, as soon as its keys are there and its accumulator has been read
+        if (lane == 0) {
+            constexpr uint32_t id_s = kInt ? idesc_i8(128, Sh::kNS, 1, 1) : idesc_e4m3(128, Sh::kNS);
+            int item = -1;
+#pragma unroll 1
+            for (int i = 0; i < count; ++i) {
+                const int stage = i % kSt, buf = i % Sh::kSBufs;
+                wait(&S.k_full[stage], (i / kSt) & 1, ok);
+                const int flags = S.info[i % kInfo].flags;
+                if (flags & kFirst) {
+                    ++item;
+                    wait(&S.q_full[item & 1], (item >> 1) & 1, ok);
+                }
+                wait(&S.s_empty[buf], ((i / Sh::kSBufs) + 1) & 1, ok);
+                tc_fence_after_sync();
+                const uint32_t a = smem_u32(kring + stage * kTileBytes), b = smem_u32(qbuf + (item & 1) * Sh::kQBytes);
 #pragma unroll
-                        for (int n = 0; n < 16; n += 4) {
-                            write_row(p, s.start, x.head, r,
-                                      make_float4(st.o[n].x, st.o[n + 1].x, st.o[n + 2].x, st.o[n + 3].x), st.z, 32 * t + n);
-                            write_row(p, s.start, x.head, r,
-                                      make_float4(st.o[n].y, st.o[n + 1].y, st.o[n + 2].y, st.o[n + 3].y), st.z,
-                                      32 * t + 16 + n);
+                for (int k = 0; k < 4; ++k)
+                    mma_ss<KIND>(tmem + buf * Sh::kNS, smem_desc_sw128(a + 32 * k), smem_desc_sw128(b + 32 * k), id_s, k > 0);
+                tc_commit(&S.s_full[buf]);
+                tc_commit(&S.k_empty[stage]);
+                if (flags & kLast) tc_commit(&S.q_empty[item & 1]);
+                mbar_arrive(&S.s_full[buf]);  // (hands on the tile's info and the rows' scales, which this thread has acquired)
+            }
+        }
+        __syncwarp();
+    } else if (warp == Sh::kWarpPV) {
+        // ---- O of each tile, added to its group's sums
+        if (lane == 0) {
+            constexpr uint32_t id_o = (kInt ? idesc_i8(128, Sh::kNP, 1, 0) : idesc_e4m3(128, Sh::kNP)) | (1u << 15) |
+                                      (1u << 16);  // both operands M/N-major
+#pragma unroll 1
+            for (int i = 0; i < count; ++i) {
+                const int stage = i % Sh::kVStages, g = i & 1;
+                wait(&S.v_full[stage], (i / Sh::kVStages) & 1, ok);
+                wait(&S.p_full[g], (i >> 1) & 1, ok);
+                tc_fence_after_sync();
+                const uint32_t a = smem_u32(vring + stage * kTileBytes), b = smem_u32(pbuf + g * Sh::kPBytes);
+                const uint32_t acc = S.accumulate[g];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss<KIND>(tmem + Sh::kO + g * Sh::kNP, smem_desc_sw128(a + 4096 * k),
+                                 weights_desc<Sh::kPRow>(b + 32 * Sh::kPRow * k), id_o, k > 0 || acc);
+                tc_commit(&S.p_empty[g]);
+                tc_commit(&S.v_empty[stage]);
+            }
+        }
+        __syncwarp();
+    } else if (warp == Sh::kWarpQ) {
+        // ---- query digits of each item, ahead of its tiles
+#pragma unroll 1
+        for (int done = 0, item = 0; done < count; ++item) {
+            const int slot = item % kItems;
+            wait(&S.item_full[slot], (item / kItems) & 1, ok);
+            const ItemInfo it = S.item[slot];
+            wait(&S.q_empty[item & 1], ((item >> 1) + 1) & 1, ok);
+            uint8_t *qb = qbuf + (item & 1) * Sh::kQBytes;
+#pragma unroll 1
+            for (int rr0 = 0; rr0 < R; rr0 += 4) {
+                float4 x[4];
+                float up[4], down[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int row = R * it.rt + rr0 + h;
+                    x[h] = make_float4(0, 0, 0, 0);
+                    if (row < it.s.rows) {
+                        const int ri = p.by_gq.quot(row);
+                        x[h] = *reinterpret_cast<const float4 *>(p.q + static_cast<int64_t>(it.s.start + ri) * p.ldq +
+                                                                 (it.head * p.GQ + row - ri * p.GQ) * kPD + 4 * lane);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const float amax = redux_max(fmaxf(fmaxf(fabsf(x[h].x), fabsf(x[h].y)), fmaxf(fabsf(x[h].z), fabsf(x[h].w))));
+                    // the row times 2^e: its largest value in [2^21, 2^22), so that three signed int8 digits hold it, or in
+                    // [2^7, 2^8), below the largest e4m3 value
+                    const int e = max(-120, min(120, (kInt ? 148 : 134) - static_cast<int>(__float_as_uint(amax) >> 23)));
+                    up[h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    down[h] = R * it.rt + rr0 + h < it.s.rows
+                                  ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                                  : 0.0f;
+                }
+                if (lane == 0) S.rowf[slot][rr0 / 4] = make_float4(down[0], down[1], down[2], down[3]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int rr = rr0 + h;
+                    // digit k of the four dimensions as one word; column of digit k of row rr: 2 kQD (rr / 2) + 2 k + rr % 2,
+                    // so that two rows' digits are neighbours
+                    const float f[4] = {x[h].x * up[h], x[h].y * up[h], x[h].z * up[h], x[h].w * up[h]};
+                    uint32_t w[Sh::kQD];
+                    if constexpr (kInt) {
+                        // (n + 0x8080) ^ 0x8080 has the signed digits d0, d1 as its low bytes, d2 above
+                        uint32_t n[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) n[d] = static_cast<uint32_t>(__float2int_rn(f[d]) + 0x8080) ^ 0x8080u;
+                        const uint32_t lo0 = __byte_perm(n[0], n[1], 0x5140), lo1 = __byte_perm(n[2], n[3], 0x5140);
+                        const uint32_t hi0 = __byte_perm(n[0], n[1], 0x0062), hi1 = __byte_perm(n[2], n[3], 0x0062);
+                        w[0] = __byte_perm(lo0, lo1, 0x5410);
+                        w[1] = __byte_perm(lo0, lo1, 0x7632);
+                        w[2] = __byte_perm(hi0, hi1, 0x5410);
+                    } else {
+                        float2 a = make_float2(f[0], f[1]), b = make_float2(f[2], f[3]);
+#pragma unroll
+                        for (int k = 0; k < Sh::kQD; ++k) {
+                            const uint32_t lo = e4m3_digit(a);
+                            w[k] = lo | e4m3_digit(b) << 16;
                         }
                     }
-                } else {
-                    const int slot = k_first > 0 ? 0 : 1;  // a range's first piece, or its last
-                    float *dst = (slot == 0 ? S.first[warp] : reinterpret_cast<float *>(my_ring)) + g * kPD + 32 * t;
 #pragma unroll
-                    for (int n = 0; n < 16; n += 4) {
-                        *reinterpret_cast<float4 *>(dst + n) =
-                            make_float4(st.o[n].x, st.o[n + 1].x, st.o[n + 2].x, st.o[n + 3].x);
-                        *reinterpret_cast<float4 *>(dst + 16 + n) =
-                            make_float4(st.o[n].y, st.o[n + 1].y, st.o[n + 2].y, st.o[n + 3].y);
+                    for (int k = 0; k < Sh::kQD; ++k)
+                        *reinterpret_cast<uint32_t *>(
+                            qb + sw128_offset(2 * Sh::kQD * (rr >> 1) + 2 * k + (rr & 1), 4 * lane)) = w[k];
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&S.q_full[item & 1]);
+                mbar_arrive(&S.item_empty[slot]);
+            }
+            done += it.tiles;
+        }
+    } else if (warp >= Sh::kHelpers) {
+        // ---- softmax group g: tiles g, g + 2, ...; thread = token of the tile and dimension of the output, rows
+        // r0 .. r0 + kRW - 1
+        const int in = tid - 32 * Sh::kHelpers, g = in / kGroup, gt = in % kGroup, w4 = warp & 3, me = tid & 127;
+        const int r0 = kRW * (gt >> 7);
+        const uint32_t lanes = static_cast<uint32_t>(w4) << 21;  // this warp's quarter of tensor memory
+        const uint32_t ts = tmem + lanes + Sh::kQD * r0, to = tmem + lanes + Sh::kO + g * Sh::kNP + 4 * r0;
+        uint8_t *my_p = pbuf + g * Sh::kPBytes;
+        float2 z[kRW / 2];
+        float o[kRW];
+        float vref = 1.0f, inv_vref = 1.0f;
+        int chain = 0, k_first = 0;
+        int handovers = 0;  // items of which both groups had parts
+#pragma unroll 1
+        for (int i = g; i < count; i += 2) {
+            const TileInfo &f = S.info[i % kInfo];
+            const int buf = i % Sh::kSBufs;
+            wait(&S.s_full[buf], (i / Sh::kSBufs) & 1, ok);
+            tc_fence_after_sync();
+            const int flags = f.flags;
+            if (flags & kGroupFirst) {
+                k_first = f.k - ((flags & kFirst) ? 0 : 1);  // the first tile that the CTA has of the item
+#pragma unroll
+                for (int r = 0; r < kRW; ++r) o[r] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kRW / 2; ++r) z[r] = make_float2(0.0f, 0.0f);
+                if (gt < R) {
+                    reinterpret_cast<float *>(S.m[g])[gt] = -INFINITY;
+                    reinterpret_cast<float *>(S.mref[g])[gt] = 0.0f;
+                }
+                any_of<kGroup>(false, g);
+            }
+            // scores of this token, in log2
+            float x[kRW];
+            {
+                const float ks = f.ks[me >> 4];
+                const float2 ks2 = make_float2(ks, ks);
+#pragma unroll
+                for (int h = 0; h < kRW / 8; ++h) {
+                    uint32_t sv[8 * Sh::kQD];
+#pragma unroll
+                    for (int e = 0; e < Sh::kQD; ++e)
+                        tmem_ld8(ts + buf * Sh::kNS + 8 * Sh::kQD * h + 8 * e, *reinterpret_cast<uint32_t(*)[8]>(sv + 8 * e));
+                    tmem_wait_ld();
+                    const float4 ra = S.rowf[f.ord % kItems][r0 / 4 + 2 * h], rb = S.rowf[f.ord % kItems][r0 / 4 + 2 * h + 1];
+                    const float2 rf[4] = {make_float2(ra.x, ra.y), make_float2(ra.z, ra.w), make_float2(rb.x, rb.y),
+                                          make_float2(rb.z, rb.w)};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t *d = sv + 2 * Sh::kQD * r;
+                        float2 t;
+                        if constexpr (kInt) {  // ((d2 2^8) + d1) 2^8 + d0
+                            const float2 up = make_float2(256.0f, 256.0f);
+                            t = make_float2(small_int(d[4]), small_int(d[5]));
+                            t = __ffma2_rn(t, up, make_float2(small_int(d[2]), small_int(d[3])));
+                            t = __ffma2_rn(t, up, make_float2(small_int(d[0]), small_int(d[1])));
+                        } else {  // d0 + (d1 + ...) / 16
+                            const float2 down = make_float2(0.0625f, 0.0625f);
+                            t = make_float2(__uint_as_float(d[8]), __uint_as_float(d[9]));
+#pragma unroll
+                            for (int k = 3; k >= 0; --k)
+                                t = __ffma2_rn(t, down, make_float2(__uint_as_float(d[2 * k]), __uint_as_float(d[2 * k + 1])));
+                        }
+                        const float2 s2 = __fmul2_rn(t, __fmul2_rn(rf[r], ks2));
+                        x[8 * h + 2 * r] = s2.x;
+                        x[8 * h + 2 * r + 1] = s2.y;
                     }
-                    if (t == 0) {
-                        S.m[warp][slot][g] = st.m;
-                        S.z[warp][slot][g] = st.z;
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.s_empty[buf]);
+            }
+            if (flags & kEdge) {
+                const Seq s = f.s;
+                const int tok = f.j0[me >> 4] + (me & 15);
+                const bool there = f.valid >> (me >> 4) & 1;
+#pragma unroll
+                for (int r = 0; r < kRW; ++r) {
+                    const int pos = s.first + p.by_gq.quot(min(R * f.rt + r0 + r, s.rows - 1));
+                    if (!there || tok > pos || (p.window > 0 && tok <= pos - p.window && tok >= p.sinks)) x[r] = -INFINITY;
+                }
+                if constexpr (!kInt) {
+                    // a weight of 0 would not undo a NaN code of a token that not every row sees: its value row is set to 0
+                    // where no row sees it (it may hold anything), and loses its NaN codes where some do, whose scores
+                    // become NaN instead
+                    bool unseen = true, hidden = false;
+#pragma unroll
+                    for (int r = 0; r < kRW; ++r) {
+                        unseen &= x[r] == -INFINITY;
+                        hidden |= x[r] == -INFINITY;
                     }
-                    if (lane == 0) {
-                        Piece pc;
-                        pc.valid = 1;
-                        pc.ends = ends;
-                        pc.s = s;
-                        pc.head = x.head;
-                        pc.rt = x.rt;
-                        pc.u0 = u0 + i - (x.k >> 1);
-                        pc.units = tile_count<1>(tiles_of<kRows>(p, s, x.rt));
-                        S.piece[warp][slot] = pc;
+                    if (hidden) {
+                        const int vs = i % Sh::kVStages;
+                        wait(&S.v_full[vs], (i / Sh::kVStages) & 1, ok);
+                        uint4 *vrow = reinterpret_cast<uint4 *>(vring + vs * kTileBytes + me * kPD);
+                        uint32_t nan = 0;
+#pragma unroll
+                        for (int k = 0; k < kPD / 16; ++k) {
+                            uint4 c = vrow[k];
+                            uint32_t *w = &c.x;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t is = unseen ? 0xFFFFFFFFu : __vcmpeq4(w[e] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                                w[e] &= ~is;
+                                nan |= is;
+                            }
+                            if (nan) vrow[k] = c;
+                        }
+                        if (nan)
+#pragma unroll
+                            for (int r = 0; r < kRW; ++r) x[r] = x[r] == -INFINITY ? x[r] : NAN;
                     }
                 }
             }
+            const float vmax = f.vmax;
+            bool flush = (flags & kGroupFirst) || chain >= (kInt ? kChainInt8 : kChainE4m3) || vmax > vref || (vmax > 0.0f && vmax < vref * kVRange);
+#pragma unroll
+            for (int h = 0; h < kRW / 4; ++h) {
+                const float4 m = S.m[g][r0 / 4 + h];
+                flush |= x[4 * h] > m.x || x[4 * h + 1] > m.y || x[4 * h + 2] > m.z || x[4 * h + 3] > m.w;
+            }
+            if (any_of<kGroup>(flush, g)) {
+                // ---- new references: each row's largest score of the tile over all 128 tokens
+#pragma unroll
+                for (int r = 0; r < kRW; ++r) {
+                    const float y = redux_max(x[r]);
+                    if (lane == 0) S.wmax[g][w4][r0 + r] = y;
+                }
+                if (chain > 0) {
+                    wait(&S.p_empty[g], ((i - 2) >> 1) & 1, ok);  // PV of this group's last tile
+                    tc_fence_after_sync();
+                    add_sums<R, KIND>(to, vref, o);
+                    tc_fence_before_sync();
+                }
+                any_of<kGroup>(false, g);  // the maxima of all warps are there
+                // each row's new reference, and what it makes of the sums so far
+                if (gt < R) {
+                    const float m = reinterpret_cast<const float *>(S.m[g])[gt];
+                    const float top = fmaxf(fmaxf(S.wmax[g][0][gt], S.wmax[g][1][gt]),
+                                            fmaxf(S.wmax[g][2][gt], S.wmax[g][3][gt]));
+                    float back = 1.0f;
+                    if (top > m) {
+                        back = ex2(m - (top + kHeadroom));
+                        reinterpret_cast<float *>(S.m[g])[gt] = reinterpret_cast<float *>(S.mref[g])[gt] = top + kHeadroom;
+                    }
+                    reinterpret_cast<float *>(S.back[g])[gt] = back;
+                }
+                any_of<kGroup>(false, g);
+                if (!(flags & kGroupFirst)) {
+#pragma unroll
+                    for (int h = 0; h < kRW / 4; ++h) {
+                        const float4 back = S.back[g][r0 / 4 + h];
+                        const float bk[4] = {back.x, back.y, back.z, back.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[4 * h + e] *= bk[e];
+                        z[2 * h] = __fmul2_rn(z[2 * h], make_float2(back.x, back.y));
+                        z[2 * h + 1] = __fmul2_rn(z[2 * h + 1], make_float2(back.z, back.w));
+                    }
+                }
+                if (vmax > 0.0f) {
+                    vref = vmax;
+                    inv_vref = recip(vmax);
+                }
+                chain = 0;
+            }
+            // weights and their digits
+            const float up = f.vs[me >> 4] * inv_vref * (kInt ? 0x1p32f : 0x1p8f);
+            const float2 up2 = make_float2(up, up);
+            wait(&S.p_empty[g], ((i >> 1) + 1) & 1, ok);  // PV of this group's last tile has read the buffer
+            uint8_t *row = my_p + me * Sh::kPRow;
+            float2 u[kRW / 2];
+#pragma unroll
+            for (int h = 0; h < kRW / 4; ++h) {
+                const float4 m = S.mref[g][r0 / 4 + h];
+                const float2 x0 = __fadd2_rn(make_float2(x[4 * h], x[4 * h + 1]), make_float2(-m.x, -m.y));
+                const float2 x1 = __fadd2_rn(make_float2(x[4 * h + 2], x[4 * h + 3]), make_float2(-m.z, -m.w));
+                const float2 w0 = make_float2(ex2(x0.x), ex2(x0.y)), w1 = make_float2(ex2(x1.x), ex2(x1.y));
+                z[2 * h] = __fadd2_rn(z[2 * h], w0);
+                z[2 * h + 1] = __fadd2_rn(z[2 * h + 1], w1);
+                u[2 * h] = __fmul2_rn(w0, up2);
+                u[2 * h + 1] = __fmul2_rn(w1, up2);
+                if constexpr (kInt)
+                    *reinterpret_cast<uint4 *>(row + (weights_chunk<Sh::kPRow>(r0 / 4 + h, me) << 4)) =
+                        make_uint4(to_u32_sat(u[2 * h].x), to_u32_sat(u[2 * h].y), to_u32_sat(u[2 * h + 1].x),
+                                   to_u32_sat(u[2 * h + 1].y));
+            }
+            if constexpr (!kInt) {
+                // column of digit k of row r: R k + r
+#pragma unroll
+                for (int k = 0; k < Sh::kVD; ++k) {
+                    uint32_t d[kRW / 4];
+#pragma unroll
+                    for (int h = 0; h < kRW / 4; ++h) {
+                        const uint32_t lo = e4m3_digit(u[2 * h]);
+                        d[h] = lo | e4m3_digit(u[2 * h + 1]) << 16;
+                    }
+                    if constexpr (R == 16)
+                        *reinterpret_cast<uint4 *>(row + (weights_chunk<128>(k, me) << 4)) = make_uint4(d[0], d[1], d[2], d[3]);
+                    else
+                        *reinterpret_cast<uint2 *>(row + (weights_chunk<128>(k >> 1, me) << 4) + 8 * (k & 1)) =
+                            make_uint2(d[0], d[1]);
+                }
+            }
+            if (gt == 0) S.accumulate[g] = chain > 0;
+            ++chain;
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_full[g]);
+
+            if (flags & kGroupLast) {
+                // ---- this group's part of the item is done
+                float zs[kRW];
+#pragma unroll
+                for (int r = 0; r < kRW / 2; ++r) {
+                    zs[2 * r] = z[r].x;
+                    zs[2 * r + 1] = z[r].y;
+                }
+                const float zw = sum_rows<kRW>(zs, lane);
+                if (lane < kRW) S.zsum[g][w4][r0 + lane] = zw;
+                wait(&S.p_empty[g], (i >> 1) & 1, ok);
+                tc_fence_after_sync();
+                add_sums<R, KIND>(to, vref, o);
+                tc_fence_before_sync();
+                chain = 0;
+                // the sums by dimension: where the weights lay, or, when the other group has the item's last tile, handed
+                // over to it once it has taken what it was handed before
+                const bool hand = !(flags & kLast);
+                if (hand) wait(&S.sum_empty, (handovers + 1) & 1, ok);
+                float *own = (hand ? handed : reinterpret_cast<float *>(my_p)) + me;
+#pragma unroll
+                for (int r = 0; r < kRW; ++r) own[(r0 + r) * kPD] = o[r];
+                any_of<kGroup>(false, g);
+                const float zr = gt < R ? (S.zsum[g][0][gt] + S.zsum[g][1][gt]) + (S.zsum[g][2][gt] + S.zsum[g][3][gt]) : 0.0f;
+                if (hand) {
+                    if (gt < R) {
+                        S.sum_z[gt] = zr;
+                        S.sum_m[gt] = reinterpret_cast<const float *>(S.m[g])[gt];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.sum_full);
+                } else {
+                    const bool both = (flags & kBoth) != 0, ends = (flags & kEnds) != 0, complete = k_first == 0 && ends;
+                    const int slot = k_first > 0 ? 0 : 1;
+                    if (both) wait(&S.sum_full, handovers & 1, ok);
+                    float *rec = p.part + static_cast<int64_t>(2 * c + slot) * rec_floats(R);
+                    if (gt < R) {
+                        // factors of the two parts, the final division included
+                        const float m0 = reinterpret_cast<const float *>(S.m[g])[gt], m1 = both ? S.sum_m[gt] : -INFINITY;
+                        const float M = fmaxf(m0, m1), ref = M == -INFINITY ? 0.0f : M;
+                        float2 fac = make_float2(ex2(m0 - ref), ex2(m1 - ref));
+                        const float zz = zr * fac.x + (both ? S.sum_z[gt] * fac.y : 0.0f);
+                        if (complete) {
+                            const float iz = recip(zz);
+                            fac = make_float2(fac.x * iz, fac.y * iz);
+                        } else {
+                            *reinterpret_cast<float2 *>(rec + R * kPD + 2 * gt) = make_float2(M, zz);
+                        }
+                        S.factors[g][gt] = fac;
+                    }
+                    any_of<kGroup>(false, g);
+                    const Seq s = f.s;
+                    const int rows = min(R, s.rows - R * f.rt);
+                    // a warp a row, four dimensions a lane
+                    const float4 *mine = reinterpret_cast<const float4 *>(my_p) + lane;
+                    const float4 *other = reinterpret_cast<const float4 *>(handed) + lane;
+#pragma unroll 2
+                    for (int r = gt >> 5; r < rows; r += kGroup / 32) {
+                        const float2 fac = S.factors[g][r];
+                        float4 t = mine[r * (kPD / 4)];
+                        t = make_float4(t.x * fac.x, t.y * fac.x, t.z * fac.x, t.w * fac.x);
+                        if (both) {
+                            const float4 y = other[r * (kPD / 4)];
+                            t = make_float4(fmaf(y.x, fac.y, t.x), fmaf(y.y, fac.y, t.y), fmaf(y.z, fac.y, t.z),
+                                            fmaf(y.w, fac.y, t.w));
+                        }
+                        const int rw = R * f.rt + r, ri = p.by_gq.quot(rw);
+                        float *dst = complete ? p.out + static_cast<int64_t>(s.start + ri) * p.ldo +
+                                                    (f.head * p.GQ + rw - ri * p.GQ) * kPD
+                                              : rec + r * kPD;
+                        *reinterpret_cast<float4 *>(dst + 4 * lane) = t;
+                    }
+                    if (both) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&S.sum_empty);
+                    }
+                }
+                if (flags & kBoth) ++handovers;
+                any_of<kGroup>(false, g);  // the sums have been read
+            }
         }
     }
+    tc_fence_before_sync();
     __syncthreads();
-
-    // ---- pieces of this CTA's warps: group a begins with a warp's last piece
-    // (a = warp) or with the first piece of warp 0 (a = -1), and goes on with
-    // the first pieces of the warps behind it until the item ends
-    const bool is_warp = lane < kWarps;
-    const unsigned first_ok = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].valid);
-    const unsigned first_ends = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][0].ends);
-    const unsigned last_ok = __ballot_sync(0xffffffffu, is_warp && S.piece[is_warp ? lane : 0][1].valid);
-    // bit 0: the first piece of warp 0, bit a + 1: the last piece of warp a
-#pragma unroll 1
-    for (unsigned groups = (first_ok & 1u) | last_ok << 1; groups != 0; groups &= groups - 1) {
-        const int a = __ffs(groups) - 2, w0 = max(a, 0), slot0 = a < 0 ? 0 : 1;
-        const Piece pc = S.piece[w0][slot0];
-        // last warp of the group: the first behind w0 whose first piece ends the item, else the last of those that have one
-        bool ends = pc.ends;
-        int w1 = w0;
-        if (!ends) {
-            const int run = __ffs(~(first_ok >> (w0 + 1))) - 1, e = __ffs(first_ends >> (w0 + 1));
-            ends = e != 0 && e <= run;
-            w1 += ends ? e : run;
-        }
-        const bool complete = a >= 0 && ends;
-        if (!complete && tid == 0) note_cut(S.cut[slot0], R, kWarps, pc.head, pc.rt, pc.s, pc.u0, pc.units);
-        const Seq s = pc.s;
-        for (int rr = warp; rr < kRows; rr += kWarps) {
-            const int row = kRows * pc.rt + rr;
-            if (row >= s.rows) break;
-            const bool mine = lane >= w0 && lane <= w1;
-            const int slot = lane == w0 ? slot0 : 0;
-            const float m = mine ? S.m[lane][slot][rr] : -INFINITY;
-            const float M = warp_max(m);
-            const float f = ex2(m - (M == -INFINITY ? 0.0f : M));
-            const float z = warp_sum(mine ? f * S.z[lane][slot][rr] : 0.0f);
-            float4 o = make_float4(0, 0, 0, 0);
-            float unused = 0.0f;
-#pragma unroll 4
-            for (int w = w0; w <= w1; ++w) {
-                const float *src = w == w0 && slot0 == 1 ? reinterpret_cast<const float *>(ring + w * kStages * kStageBytes)
-                                                         : S.first[w];
-                add_scaled(o, unused, __shfl_sync(0xffffffffu, f, w),
-                           *reinterpret_cast<const float4 *>(src + rr * kPD + 4 * lane), 0.0f);
-            }
-            if (complete) {
-                write_row(p, s.start, pc.head, row, o, z, 4 * lane);
-            } else {
-                float *rec = p.part + static_cast<int64_t>(2 * c + slot0) * rec_floats(kRows);
-                *reinterpret_cast<float4 *>(rec + rr * kPD + 4 * lane) = o;
-                if (lane == 0) *reinterpret_cast<float2 *>(rec + kRows * kPD + 2 * rr) = make_float2(M, z);
-            }
-        }
-    }
-
-    __syncthreads();
-    merge_cut_items<kRows, kThreads>(p, S.cut, S.last, nullptr);
+    tc_fence_after_sync();
+    if (warp == Sh::kWarpQK) tmem_dealloc(tmem, Sh::kTmemCols);
+    merge_cut_items<R, Sh::kThreads>(p, S.cut, S.last, reinterpret_cast<float *>(pbuf));
     pdl_launch_dependents();
 }
 
-template <int KIND>
-cudaError_t launch_split(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int ctas, cudaStream_t s) {
+template <int R, int KIND>
+cudaError_t launch_rows(const AttnParams &p, const CacheMaps &maps, int ctas, cudaStream_t s) {
     static DeviceOnce once;
     int dev = 0;
     cudaError_t e = current_device(&dev);
     if (e != cudaSuccess) return e;
     e = once.run(dev, [] {
-        return cudaFuncSetAttribute(attn_split_paged_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kSplitSmem));
+        return cudaFuncSetAttribute(attn_paged_kernel<R, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(attn_smem<R, KIND>()));
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_split_paged_kernel<KIND>, dim3(ctas), kThreads, kSplitSmem, s, p, km, vm);
+    return launch_pdl(attn_paged_kernel<R, KIND>, dim3(ctas), Shape<R, KIND>::kThreads, attn_smem<R, KIND>(), s, p, maps);
 }
 
 }  // namespace
 
-size_t attention_paged_workspace_bytes(int Hq, int Hkv, int num_sms) {
-    (void)Hq;
-    (void)Hkv;
+size_t attention_paged_workspace_bytes(int num_sms) {
     // the counters, and two partial records a CTA (one CTA per SM)
     return kMaxCtas * sizeof(int) + static_cast<size_t>(2) * std::min(num_sms, kMaxCtas) * rec_floats(kMaxRows) * sizeof(float);
 }
@@ -509,7 +974,7 @@ cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s
     CacheMaps maps;
     const uint64_t cache_rows = static_cast<uint64_t>(A.cache.n_pages) * A.cache.Hkv * A.cache.page_size;
     // boxes of more blocks than the cache holds are never used, and not made
-    for (int i = 0; i < (A.cache.kind == TERN_KV_INT8 ? 4 : 1); ++i) {
+    for (int i = 0; i < 4; ++i) {
         const uint32_t box = static_cast<uint32_t>(std::min<uint64_t>(kPB << i, cache_rows));
         if (!make_u8_tmap_2d(&maps.k[i], A.cache.k_codes, kPD, cache_rows, kPD, kPD, box) ||
             !make_u8_tmap_2d(&maps.v[i], A.cache.v_codes, kPD, cache_rows, kPD, kPD, box)) {
@@ -520,13 +985,20 @@ cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s
     const int64_t span = A.window > 0 ? std::min<int64_t>(A.batch.max_ctx, static_cast<int64_t>(A.window) + A.sinks + 32)
                                       : A.batch.max_ctx;
     const int64_t rows = std::min<int64_t>(static_cast<int64_t>(std::min(A.batch.max_rows, A.batch.T)) * p.GQ, 1 << 30);
-    if (A.cache.kind == TERN_KV_INT8)
-        return launch_attention_tc(p, maps, static_cast<int>(rows), span, A.num_sms, s);
+    const bool int8 = A.cache.kind == TERN_KV_INT8;
+    // Items of 8, 16 or, of int8, 32 rows (e4m3's digits take five columns of tensor memory a row).  In us with 8 / 16 /
+    // 32 rows, and e4m3 with 8 / 16: one token, context 65536, of 40 heads on 8 33.0 / - / 44.4, 34.2 / 36.5, of 128
+    // heads on 8 47.9 / 42.2 / 49.1; three sequences of 2 drafted tokens, 40 heads, context 8191 26.0 / 25.0 / 28.6, of
+    // 16 tokens 76 / 55 / 56, 80 / 62; a prompt's last 2048 of 4096 tokens 1042 / 780 / 539, 1149 / 1046.
+    const int R = rows <= 8 ? 8 : int8 && rows > 16 ? 32 : 16;
     // one CTA per SM, fewer when the tiles are few
-    const int64_t units = std::min<int64_t>(A.batch.B, A.batch.T) * A.cache.Hkv * ceil_div(rows, kRows) * ceil_div(span, kPB);
-    int64_t ctas = std::min<int64_t>(A.num_sms, ceil_div(units, kWarps));
-    ctas = std::max<int64_t>(1, std::min<int64_t>(ctas, kMaxCtas));
-    return launch_split<TERN_KV_E4M3>(p, maps.k[0], maps.v[0], static_cast<int>(ctas), s);
+    const int64_t tiles = std::min<int64_t>(A.batch.B, A.batch.T) * A.cache.Hkv * ceil_div(rows, R) * ceil_div(span, kTok);
+    const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({tiles, A.num_sms, kMaxCtas})));
+    if (int8)
+        return R == 8    ? launch_rows<8, TERN_KV_INT8>(p, maps, ctas, s)
+               : R == 16 ? launch_rows<16, TERN_KV_INT8>(p, maps, ctas, s)
+                         : launch_rows<32, TERN_KV_INT8>(p, maps, ctas, s);
+    return R == 8 ? launch_rows<8, TERN_KV_E4M3>(p, maps, ctas, s) : launch_rows<16, TERN_KV_E4M3>(p, maps, ctas, s);
 }
 
 }  // namespace tern

@@ -1,10 +1,10 @@
-// tern_paged_attention.cuh -- what the two kernels of the paged attention
-// share: the items of a batch, their visible blocks of 16 tokens, and the line
-// of all their tiles that the grid divides evenly.
+// tern_paged_attention.cuh -- how the paged attention divides its work: the
+// items of a batch, their visible blocks of 16 tokens, the line of all their
+// tiles that the grid divides evenly, and the merging of divided items.
 //
 // The rows of one sequence that share a KV head (its tokens times the query
 // heads of the group) are taken R at a time: an item.  An item's work is its
-// visible blocks of 16 tokens (one scale each), TB blocks to a tile.  All
+// visible blocks of 16 tokens (one scale each), eight blocks to a tile.  All
 // tiles of all items form one line (by sequence, head, row tile, tile), cut
 // into equal ranges, so that uneven contexts fill the GPU evenly; the lengths
 // are read on the device.
@@ -14,6 +14,7 @@
 
 namespace tern {
 
+constexpr int kTB = 8;           // blocks of a tile
 constexpr int kMaxRows = 32;     // rows of an item, at most
 constexpr int kMaxCtas = 1024;   // CTAs of a launch (counters at the workspace's start)
 // A partial record: [rows][kPD] sums, then (m, z) of each row.
@@ -81,15 +82,14 @@ __device__ __forceinline__ Tiles tiles_of(const AttnParams &p, const Seq &s, int
 
 // Tiles of one KV head of a sequence (an item that sees nothing still counts
 // one: its rows are written as 0).
-template <int TB>
 __device__ __forceinline__ int tile_count(const Tiles &t) {
-    return max(1, (t.n + TB - 1) / TB);
+    return max(1, (t.n + kTB - 1) / kTB);
 }
-template <int R, int TB>
+template <int R>
 __device__ __forceinline__ long long head_units(const AttnParams &p, const Seq &s) {
     long long u = 0;
 #pragma unroll 1
-    for (int rt = 0; rt * R < s.rows; ++rt) u += tile_count<TB>(tiles_of<R>(p, s, rt));
+    for (int rt = 0; rt * R < s.rows; ++rt) u += tile_count(tiles_of<R>(p, s, rt));
     return u;
 }
 
@@ -125,17 +125,16 @@ struct Ranges {
 };
 
 // A place on the line: tile k of an item.
-template <int TB>
 struct Cursor {
     int b, head, rt, k;
     int ord;  // items passed since the range's first
     Seq s;
     Tiles tl;
-    __device__ __forceinline__ int units() const { return tile_count<TB>(tl); }
+    __device__ __forceinline__ int units() const { return tile_count(tl); }
 };
 
-template <int R, int TB, typename SeqOf>
-__device__ __forceinline__ void advance(const AttnParams &p, Cursor<TB> &x, int n, SeqOf seq_of) {
+template <int R, typename SeqOf>
+__device__ __forceinline__ void advance(const AttnParams &p, Cursor &x, int n, SeqOf seq_of) {
     x.k += n;
 #pragma unroll 1
     while (x.k >= x.units()) {
@@ -173,7 +172,7 @@ struct Line {
 };
 
 // (All threads of the CTA, at least kLineThreads; holds several __syncthreads.)
-template <int R, int TB>
+template <int R>
 __device__ __forceinline__ Line make_line(const AttnParams &p, LineShared &S) {
     const PagedView &v = p.v;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -191,16 +190,16 @@ __device__ __forceinline__ Line make_line(const AttnParams &p, LineShared &S) {
     if (counts && L.per > 1) {
 #pragma unroll 1
         for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b)
-            mine += v.Hkv * head_units<R, TB>(p, sequence(p, b));
+            mine += v.Hkv * head_units<R>(p, sequence(p, b));
     } else if (counts && !many) {
-        S.head[tid] = static_cast<int>(head_units<R, TB>(p, s));
+        S.head[tid] = static_cast<int>(head_units<R>(p, s));
     } else if (counts) {
 #pragma unroll 1
         for (int b = warp; b < v.B; b += kLineThreads / 32) {
             const Seq t = S.seq[b];
             int n = 0;
 #pragma unroll 1
-            for (int rt = lane; rt * R < t.rows; rt += 32) n += tile_count<TB>(tiles_of<R>(p, t, rt));
+            for (int rt = lane; rt * R < t.rows; rt += 32) n += tile_count(tiles_of<R>(p, t, rt));
             n = warp_sum_int(n);
             if (lane == 0) S.head[b] = n;
         }
@@ -230,11 +229,11 @@ __device__ __forceinline__ Line make_line(const AttnParams &p, LineShared &S) {
 }
 
 // The place of line index u < total (warp-collective).
-template <int R, int TB, typename SeqOf>
-__device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const LineShared &S, const Line &L, long long u,
+template <int R, typename SeqOf>
+__device__ __forceinline__ Cursor find_place(const AttnParams &p, const LineShared &S, const Line &L, long long u,
                                                  SeqOf seq_of) {
     const int lane = threadIdx.x & 31;
-    Cursor<TB> cur;
+    Cursor cur;
     int lo = 0;  // the last thread whose sequences begin at or before u
 #pragma unroll 1
     for (int i = 0; i < kLineThreads / 32 && 32 * i * L.per < p.v.B; ++i) {
@@ -246,7 +245,7 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
 #pragma unroll 1
     for (;; ++b) {
         cur.s = seq_of(b);
-        ph = L.per == 1 ? S.head[b] : head_units<R, TB>(p, cur.s);
+        ph = L.per == 1 ? S.head[b] : head_units<R>(p, cur.s);
         if (off < ph * p.v.Hkv || b + 1 == p.v.B) break;  // (the second: lengths that changed under the kernel end here)
         off -= ph * p.v.Hkv;
     }
@@ -256,7 +255,7 @@ __device__ __forceinline__ Cursor<TB> find_place(const AttnParams &p, const Line
     // the row tile, 32 at a time
 #pragma unroll 1
     for (int rt0 = 0;; rt0 += 32) {
-        const int rt = rt0 + lane, n = rt * R < cur.s.rows ? tile_count<TB>(tiles_of<R>(p, cur.s, rt)) : 0;
+        const int rt = rt0 + lane, n = rt * R < cur.s.rows ? tile_count(tiles_of<R>(p, cur.s, rt)) : 0;
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -306,13 +305,13 @@ struct CutItem {
 
 // item: the CTA's first (a = 0) or last (a = 1) item, whose first tile has line
 // index u0.
-__device__ __forceinline__ void note_cut(CutItem &x, const Ranges &ranges, int per_cta, int head, int rt, const Seq &s,
+__device__ __forceinline__ void note_cut(CutItem &x, const Ranges &ranges, int head, int rt, const Seq &s,
                                          long long u0, int units) {
     x.head = head;
     x.rt = rt;
     x.s = s;
-    x.first = ranges.owner(u0) / per_cta;
-    x.parts = ranges.owner(u0 + units - 1) / per_cta - x.first + 1;
+    x.first = ranges.owner(u0);
+    x.parts = ranges.owner(u0 + units - 1) - x.first + 1;
     x.valid = 1;
 }
 
@@ -399,11 +398,5 @@ __device__ __forceinline__ void merge_cut_items(const AttnParams &p, const CutIt
         }
     }
 }
-
-// The int8 form on the 5th-generation tensor cores (tern_paged_attention_tc.cu):
-// max_rows: about the most rows (tokens times heads of a group) of a sequence,
-// span: about the most tokens one of them sees.
-cudaError_t launch_attention_tc(const AttnParams &p, const CacheMaps &maps, int max_rows, int64_t span, int num_sms,
-                                cudaStream_t s);
 
 }  // namespace tern
