@@ -37,18 +37,29 @@
 // happens a few times per item (26 of int8's 32 bits remain; block scales may
 // cost 8 more).
 //
-// One CTA per SM.  Warps of their own copy K and V, issue QK, issue PV and
-// make the query digits (issuing takes a thread some 450 cycles a product; one
-// warp for both took longer than a tile's bytes).  Two softmax groups (thread =
-// token of S, dimension of O; with 32 rows each group is two warpgroups of 16)
-// take the tiles in turn, each with its own accumulators, references and weight
-// buffer, so that one group's waits, fences and barriers pass under the other's
-// arithmetic; what they have of an item is put together at its end.  A tile is
-// eight visible blocks of 16 tokens of an item, from anywhere in the sequence,
-// so sinks and a window fill whole tiles.  Everything runs ahead across items:
-// K and V by rings of their own (a K stage is free after QK, a V stage after
-// PV), QK of the next tiles before PV of this one, the next item's digits while
-// this one's tiles are worked off.
+// One CTA per SM.  Warps of their own look the tiles up, copy K, copy V, issue
+// QK, issue PV and make the query digits: a thread takes some 450 cycles to
+// issue a product, and look-up and K's copies in one warp took 1570 cycles a
+// tile of 16-token pages, more than the 1430 in which memory delivers it (24
+// ragged sequences 114 us; with a warp for each 98).  With 32 rows one warp
+// looks up and copies, which leaves 96 registers a thread.  Two softmax groups
+// (thread = token of S, dimension of O; with 32 rows each group is two
+// warpgroups of 16) take the tiles in turn, each with its own accumulators,
+// references and weight buffer, so that one group's waits, fences and barriers
+// pass under the other's arithmetic; what they have of an item is put together
+// at its end.  A tile is eight visible blocks of 16 tokens of an item, from
+// anywhere in the sequence, so sinks and a window fill whole tiles.  Everything
+// runs ahead across items: K and V by rings of their own (a K stage is free
+// after QK, a V stage after PV), QK of the next tiles before PV of this one, the
+// next item's digits while this one's tiles are worked off.
+//
+// Measured (device time; the floor is the codes at the measured copy rate): 24
+// sequences of 24000 to 40000 tokens, 40 heads on 8, 98 us of 86 (e4m3 and
+// int8, 16-token pages); one of 65536 33.4 of 20.5, of 4096 12.9 of 1.3 (some 8
+// us are launch, look-up and the merging of divided items); 16 sequences of
+// which a window and sinks show 4100 tokens 34 of 20.7; three sequences of 16
+// drafted tokens 56 of 8.0 and a prompt's 2048 rows of 4096 tokens 540 of 79:
+// there some 20 instructions an element of the softmax and the ends of items.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -63,8 +74,10 @@ namespace {
 
 constexpr int kTok = kTB * kPB;           // 128 tokens
 constexpr int kTileBytes = kTok * kPD;    // 16 KB of K or V codes
-constexpr int kInfo = 16;                 // tile infos kept: K's ring runs at most kStages + kSBufs + 2 tiles ahead of the softmax
-constexpr int kItems = 8;                 // items kept for the query warp, and whose score scales are kept
+constexpr int kInfo = 16;                 // tile infos kept: the copies want at most kStages + kSBufs + 2 tiles ahead of the softmax
+constexpr int kItems = 16;                // items kept for the query warp, and whose score scales are kept.  (Tile t's item, which
+                                          // may be item t, is noted before the scales of t - 11 are: at least 10, or the
+                                          // look-up waits for digits that wait for it)
 constexpr float kHeadroom = 6.0f;         // a new reference lies this far (log2) above the largest score
 constexpr int kChainInt8 = 256;           // tiles summed in int32: 256 * 128 * 255 * 127 < 2^31
 constexpr int kChainE4m3 = 16;            // tiles summed in fp32 inside the tensor cores (16 or 64: the same time)
@@ -78,9 +91,10 @@ struct Shape {
     static constexpr int kHelpers = R == 32 ? 4 : 8;  // warps in front of the softmax warps
     static constexpr int kThreads = 32 * kHelpers + 2 * kHalves * 128;
     static constexpr int kGroup = 128 * kHalves;      // threads of a softmax group
-    // warps: copies of K (of K and V with 4 helpers), of V, issue of QK, of PV, query digits
-    static constexpr int kWarpK = 0, kWarpV = kHelpers == 8 ? 1 : -1, kWarpQK = kHelpers == 8 ? 2 : 1,
-                         kWarpPV = kHelpers == 8 ? 3 : 2, kWarpQ = kHelpers == 8 ? 4 : 3;
+    // warps: look-up of the tiles (with 4 helpers their copies too), copies of K, of V, issue of QK, of PV, query digits
+    static constexpr bool kCopyWarps = kHelpers == 8;
+    static constexpr int kWarpLook = 0, kWarpK = kCopyWarps ? 1 : -1, kWarpV = kCopyWarps ? 2 : -1,
+                         kWarpQK = kCopyWarps ? 3 : 1, kWarpPV = kCopyWarps ? 4 : 2, kWarpQ = kCopyWarps ? 5 : 3;
     static constexpr int kSBufs = R == 32 ? 2 : 4;    // S accumulators
     static constexpr int kQD = kInt ? 3 : 5;          // digits of a query, columns of S per row
     static constexpr int kVD = kInt ? 4 : 5;         // digits of a weight, columns of O per row
@@ -140,7 +154,7 @@ struct AttnShared {
     float2 factors[2][R];             // of the parts at an item's end
     LineShared line;
     uint64_t k_full[Sh::kStages], k_empty[Sh::kStages], v_full[Sh::kVStages], v_empty[Sh::kVStages];
-    uint64_t info_full[kInfo], item_full[kItems], item_empty[kItems];
+    uint64_t info_full[kInfo], scales_full[kInfo], info_empty[kInfo], item_full[kItems], item_empty[kItems];
     uint64_t s_full[Sh::kSBufs], s_empty[Sh::kSBufs], p_full[2], p_empty[2], q_full[2], q_empty[2], sum_full, sum_empty;
     CutItem cut[2];
     uint32_t tmem;
@@ -277,30 +291,83 @@ __device__ __forceinline__ void add_sums(uint32_t taddr, float vref, float (&o)[
     }
 }
 
-// Look-up of a range's tiles, and K's copies (with COPY_V, V's too): writes the
-// infos of the items and tiles.
-template <int R, int KIND, bool COPY_V, typename SeqOf>
-__device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *kring,
-                                          uint8_t *vring, const Line &L, const Ranges &ranges, long long u0, int count,
-                                          SeqOf seq_of) {
+// Copies of tile i's keys, values or both, by its info; lanes 0-7 a block each.
+template <int R, int KIND, bool K, bool V>
+__device__ __forceinline__ void copy_tile(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *kring, uint8_t *vring, int i,
+                                          bool &ok) {
+    const int lane = threadIdx.x & 31, at = lane * kPB * kPD;
+    const int ik = i % Shape<R, KIND>::kStages, iv = i % Shape<R, KIND>::kVStages;
+    const TileInfo &f = S.info[i % kInfo];
+    const int size = lane < kTB ? f.size[lane] : -1, row = lane < kTB ? f.row[lane] : 0;
+    const uint32_t bytes = __popc(f.valid) * kPB * kPD;
+    if (K) {
+        wait(&S.k_empty[ik], ((i / Shape<R, KIND>::kStages) + 1) & 1, ok);
+        if (lane == 0) mbar_arrive_expect_tx(&S.k_full[ik], bytes);
+        __syncwarp();
+        if (size >= 0) tma_load_2d_nohint(kring + ik * kTileBytes + at, &maps.k[size], 0, row, &S.k_full[ik]);
+    }
+    if (V) {
+        wait(&S.v_empty[iv], ((i / Shape<R, KIND>::kVStages) + 1) & 1, ok);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&S.v_full[iv], bytes);
+            mbar_arrive(&S.info_empty[i % kInfo]);  // (the softmax is done with a tile only after K's copy)
+        }
+        __syncwarp();
+        if (size >= 0) tma_load_2d_nohint(vring + iv * kTileBytes + at, &maps.v[size], 0, row, &S.v_full[iv]);
+    }
+}
+
+// Before a CTA that copies ends: no copy is in flight, even after a wait that ran out.
+template <int R, int KIND, bool K, bool V>
+__device__ __forceinline__ void copies_land(AttnShared<R, KIND> &S, int count) {
     constexpr int kSt = Shape<R, KIND>::kStages, kVSt = Shape<R, KIND>::kVStages;
+    bool land = true;
+    if (K)
+#pragma unroll 1
+        for (int i = max(0, count - kSt); i < count; ++i) wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
+    if (V)
+#pragma unroll 1
+        for (int i = max(0, count - kVSt); i < count; ++i) wait(&S.v_full[i % kVSt], (i / kVSt) & 1, land);
+}
+
+// All copies of K, or of V.
+template <int R, int KIND, bool K>
+__device__ __forceinline__ void copy_codes(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *kring, uint8_t *vring,
+                                           int count) {
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        wait(&S.info_full[i % kInfo], (i / kInfo) & 1, ok);
+        copy_tile<R, KIND, K, !K>(maps, S, kring, vring, i, ok);
+    }
+    copies_land<R, KIND, K, !K>(S, count);
+}
+
+// Look-up of a range's tiles: writes the infos of the items and tiles.  Four
+// tiles at a time (lane = 8 * tile + block), in three steps that overlap, so
+// that no load is waited for while another could be on its way: page numbers;
+// places and masks, which the copies start from, and loads of the scales; the
+// scales, and then, without warps for them, the copies.
+template <int R, int KIND, typename SeqOf>
+__device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *kring,
+                                        uint8_t *vring, const Line &L, const Ranges &ranges, long long u0, int count,
+                                        SeqOf seq_of) {
     const PagedView &v = p.v;
     const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
     bool ok = true;
-    // four tiles at a time (lane = 8 * tile + block): a batch is looked up while the one before is copied
     Cursor cur = find_place<R>(p, S.line, L, u0, seq_of);
     const int k_first = cur.k;
     if (lane == 0) S.first_item = {cur.head, cur.rt, cur.units(), cur.s};
-    int step = sub, bi = -1, j0 = 0;
+    int step = sub, page = -1, in_page = 0, j0 = 0;
     float ks = 0.0f, vs = 0.0f;
 #pragma unroll 1
-    for (int i0 = 0; i0 < count + 4; i0 += 4) {
-        const int b_now = bi, j0_now = j0;
-        const float ks_now = ks, vs_now = vs;
+    for (int i0 = 0; i0 < count + 8; i0 += 4) {
         const Cursor it = cur;
-        bi = -1;
-        ks = vs = 0.0f;
-        if (i0 + sub < count) {  // this lane's block of tile i0 + sub
+        const int page_now = page, in_page_now = in_page, j0_now = j0;
+        const float ks_now = ks, vs_now = vs;
+        // ---- tiles i0 ..: page numbers
+        page = -1;
+        if (i0 + sub < count) {
             advance<R>(p, cur, step, seq_of);
             step = 4;
             if (j == 0 && (cur.k == 0 || i0 + sub == 0)) {
@@ -314,55 +381,50 @@ __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &
             }
             const int kb = kTB * cur.k + j;
             if (kb < cur.tl.n) {
-                const int blk = cur.tl.block(kb);
+                const int blk = cur.tl.block(kb), e = v.by_bpp.quot(blk);
                 j0 = blk * kPB;
-                const int64_t x = block_index(v, cur.b, blk);
-                if (x >= 0) {
-                    bi = static_cast<int>(x) + cur.head * v.bpp;
-                    ks = v.ks[bi];
-                    vs = v.vs[bi];
-                }
+                in_page = blk - e * v.bpp;
+                if (e < v.pages_ld) page = v.pages[static_cast<int64_t>(cur.b) * v.pages_ld + e];
             }
         }
         __syncwarp();
-        if (i0 == 0) continue;
-        const unsigned there = __ballot_sync(0xffffffffu, b_now >= 0);
-        // runs of blocks that lie behind one another in the cache: one copy each for 8, 4, 2 or 1 of them
-        // (copies of 16 rows: 2150 cycles a tile, of 64 rows 1690)
-        const int before = __shfl_up_sync(0xffffffffu, b_now, 1);
-        const unsigned follows = __ballot_sync(0xffffffffu, b_now >= 0 && b_now == before + 1) >> (8 * sub);
-        int size = 0;  // log2 of the blocks this lane copies, -1: another lane does
-        if ((follows & 0xFEu) == 0xFEu) size = 3;
-        else if ((follows >> (j & 4) & 0xEu) == 0xEu) size = 2;
-        else if (follows >> (j & 6) & 2u) size = 1;
-        if (b_now < 0 || (j & ((1 << size) - 1))) size = -1;
-        // masks: a block whose tokens not every row sees, or that is missing
-        const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
-        const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
-        const bool whole = b_now >= 0 && j0_now + kPB - 1 <= p_min &&
-                           (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
-        const unsigned not_whole = __ballot_sync(0xffffffffu, !whole);
-        float vmax = vs_now;
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-#pragma unroll 1
-        for (int e = 0; e < 4 && i0 - 4 + e < count; ++e) {
-            const int i = i0 - 4 + e, stage = i % kSt;
-            wait(&S.k_empty[stage], ((i / kSt) + 1) & 1, ok);
-            if (sub == e) {
+        // ---- tiles i0 - 4 ..: places and masks
+        if (i0 >= 4) {
+            const int i = i0 - 4 + sub;
+            const int bi = page_now >= 0 && page_now < v.n_pages ? (page_now * v.Hkv + it.head) * v.bpp + in_page_now : -1;
+            ks = vs = 0.0f;
+            if (bi >= 0) {
+                ks = v.ks[bi];
+                vs = v.vs[bi];
+            }
+            const unsigned there = __ballot_sync(0xffffffffu, bi >= 0) >> (8 * sub) & 255;
+            // runs of blocks that lie behind one another in the cache: one copy each for 8, 4, 2 or 1 of them
+            // (copies of 16 rows: 2150 cycles a tile, of 64 rows 1690)
+            const int before = __shfl_up_sync(0xffffffffu, bi, 1);
+            const unsigned follows = __ballot_sync(0xffffffffu, bi >= 0 && bi == before + 1) >> (8 * sub);
+            int size = 0;  // log2 of the blocks that this block's copy takes, -1: another's does
+            if ((follows & 0xFEu) == 0xFEu) size = 3;
+            else if ((follows >> (j & 4) & 0xEu) == 0xEu) size = 2;
+            else if (follows >> (j & 6) & 2u) size = 1;
+            if (bi < 0 || (j & ((1 << size) - 1))) size = -1;
+            // masks: a block whose tokens not every row sees, or that is missing
+            const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
+            const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
+            const bool whole = bi >= 0 && j0_now + kPB - 1 <= p_min &&
+                               (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
+            const unsigned not_whole = __ballot_sync(0xffffffffu, !whole) >> (8 * sub) & 255;
+            if (i < count) {
                 TileInfo &f = S.info[i % kInfo];
-                f.ks[j] = ks_now;
-                f.vs[j] = vs_now;
+                wait(&S.info_empty[i % kInfo], ((i / kInfo) + 1) & 1, ok);
                 f.j0[j] = j0_now;
-                f.row[j] = b_now * kPB;
+                f.row[j] = bi * kPB;
                 f.size[j] = size;
                 if (j == 0) {
                     const int since = min(it.k, i), left = min(it.units() - 1 - it.k, count - 1 - i);
-                    f.valid = there >> (8 * e) & 255;
+                    f.valid = there;
                     f.flags = (since == 0 ? kFirst : 0) | (left == 0 ? kLast : 0) | (since < 2 ? kGroupFirst : 0) |
-                              (left < 2 ? kGroupLast : 0) | (since + left > 0 ? kBoth : 0) |
-                              ((not_whole >> (8 * e) & 255) ? kEdge : 0) | (it.k + 1 == it.units() ? kEnds : 0);
-                    f.vmax = vmax;
+                              (left < 2 ? kGroupLast : 0) | (since + left > 0 ? kBoth : 0) | (not_whole ? kEdge : 0) |
+                              (it.k + 1 == it.units() ? kEnds : 0);
                     f.head = it.head;
                     f.rt = it.rt;
                     f.k = it.k;
@@ -371,22 +433,26 @@ __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &
                     f.s = it.s;
                 }
             }
-            const uint32_t bytes = __popc(there >> (8 * e) & 255) * kPB * kPD;
-            const int at = j * kPB * kPD;
             __syncwarp();
-            if (lane == 8 * e) {
-                mbar_arrive_expect_tx(&S.k_full[stage], bytes);
-                mbar_arrive(&S.info_full[i % kInfo]);
+            if (j == 0 && i < count) mbar_arrive(&S.info_full[i % kInfo]);
+        }
+        // ---- tiles i0 - 8 ..: scales
+        if (i0 >= 8) {
+            const int i = i0 - 8 + sub;
+            float vmax = vs_now;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+            if (i < count) {
+                TileInfo &f = S.info[i % kInfo];
+                f.ks[j] = ks_now;
+                f.vs[j] = vs_now;
+                if (j == 0) f.vmax = vmax;
             }
             __syncwarp();
-            if (sub == e && size >= 0) tma_load_2d_nohint(kring + stage * kTileBytes + at, &maps.k[size], 0, b_now * kPB, &S.k_full[stage]);
-            if (COPY_V) {
-                const int vs = i % kVSt;
-                wait(&S.v_empty[vs], ((i / kVSt) + 1) & 1, ok);
-                if (lane == 8 * e) mbar_arrive_expect_tx(&S.v_full[vs], bytes);
-                __syncwarp();
-                if (sub == e && size >= 0)
-                    tma_load_2d_nohint(vring + vs * kTileBytes + at, &maps.v[size], 0, b_now * kPB, &S.v_full[vs]);
+            if (j == 0 && i < count) mbar_arrive(&S.scales_full[i % kInfo]);
+            if constexpr (!Shape<R, KIND>::kCopyWarps) {
+#pragma unroll 1
+                for (int e = i0 - 8; e < min(i0 - 4, count); ++e) copy_tile<R, KIND, true, true>(maps, S, kring, vring, e, ok);
             }
         }
     }
@@ -398,36 +464,7 @@ __device__ __forceinline__ void copy_keys(const AttnParams &p, const CacheMaps &
     // (the last tile's item, as the lane that looked it up has it: cut if it goes on and began in this range)
     if (j == 0 && sub == (count - 1) % 4 && cur.k + 1 < cur.units() && cur.k <= count - 1)
         note_cut(S.cut[1], ranges, cur.head, cur.rt, cur.s, u0 + count - 1 - cur.k, cur.units());
-    // no copy is in flight when the CTA ends, even after a wait that ran out
-    bool land = true;
-#pragma unroll 1
-    for (int i = max(0, count - kSt); i < count; ++i) wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
-    if (COPY_V)
-#pragma unroll 1
-        for (int i = max(0, count - kVSt); i < count; ++i) wait(&S.v_full[i % kVSt], (i / kVSt) & 1, land);
-}
-
-// V's copies, by the tiles' infos; lanes 0-7 a block each.
-template <int R, int KIND>
-__device__ __forceinline__ void copy_values(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *vring, int count) {
-    constexpr int kSt = Shape<R, KIND>::kVStages;
-    const int lane = threadIdx.x & 31;
-    bool ok = true;
-#pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-        const int stage = i % kSt;
-        wait(&S.info_full[i % kInfo], (i / kInfo) & 1, ok);
-        const TileInfo &f = S.info[i % kInfo];
-        const int size = lane < kTB ? f.size[lane] : -1, row = lane < kTB ? f.row[lane] : 0;
-        wait(&S.v_empty[stage], ((i / kSt) + 1) & 1, ok);
-        if (lane == 0) mbar_arrive_expect_tx(&S.v_full[stage], __popc(f.valid) * kPB * kPD);
-        __syncwarp();
-        if (size >= 0)
-            tma_load_2d_nohint(vring + stage * kTileBytes + lane * kPB * kPD, &maps.v[size], 0, row, &S.v_full[stage]);
-    }
-    bool land = true;
-#pragma unroll 1
-    for (int i = max(0, count - kSt); i < count; ++i) wait(&S.v_full[i % kSt], (i / kSt) & 1, land);
+    if constexpr (!Shape<R, KIND>::kCopyWarps) copies_land<R, KIND, true, true>(S, count);
 }
 
 template <int KIND>
@@ -477,7 +514,11 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
         }
         mbar_init(&S.sum_full, 4 * Sh::kHalves);
         mbar_init(&S.sum_empty, 4 * Sh::kHalves);
-        for (int i = 0; i < kInfo; ++i) mbar_init(&S.info_full[i], 1);
+        for (int i = 0; i < kInfo; ++i) {
+            mbar_init(&S.info_full[i], 1);
+            mbar_init(&S.scales_full[i], 1);
+            mbar_init(&S.info_empty[i], 4 * Sh::kHalves + 1);
+        }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&S.item_full[i], 1);
             mbar_init(&S.item_empty[i], 1);
@@ -507,11 +548,13 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
     const uint32_t tmem = S.tmem;
 
     if (count == 0) {
+    } else if (warp == Sh::kWarpLook) {
+        look_up<R, KIND>(p, maps, S, kring, vring, L, ranges, u0, count,
+                         [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); });
     } else if (warp == Sh::kWarpK) {
-        auto seq_of = [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); };
-        copy_keys<R, KIND, (Sh::kWarpV < 0)>(p, maps, S, kring, vring, L, ranges, u0, count, seq_of);
+        copy_codes<R, KIND, true>(maps, S, kring, vring, count);
     } else if (warp == Sh::kWarpV) {
-        copy_values<R, KIND>(maps, S, vring, count);
+        copy_codes<R, KIND, false>(maps, S, kring, vring, count);
     } else if (warp == Sh::kWarpQK) {
         // ---- S of each tile, as soon as its keys are there and its accumulator has been read
         if (lane == 0) {
@@ -521,6 +564,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
             for (int i = 0; i < count; ++i) {
                 const int stage = i % kSt, buf = i % Sh::kSBufs;
                 wait(&S.k_full[stage], (i / kSt) & 1, ok);
+                wait(&S.scales_full[i % kInfo], (i / kInfo) & 1, ok);
                 const int flags = S.info[i % kInfo].flags;
                 if (flags & kFirst) {
                     ++item;
@@ -586,14 +630,18 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                 }
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const float amax = redux_max(fmaxf(fmaxf(fabsf(x[h].x), fabsf(x[h].y)), fmaxf(fabsf(x[h].z), fabsf(x[h].w))));
+                    // (the largest bits: those of a NaN or an infinity lie above all others)
+                    const uint32_t amax = __reduce_max_sync(
+                        0xffffffffu, max(max(__float_as_uint(fabsf(x[h].x)), __float_as_uint(fabsf(x[h].y))),
+                                         max(__float_as_uint(fabsf(x[h].z)), __float_as_uint(fabsf(x[h].w)))));
                     // the row times 2^e: its largest value in [2^21, 2^22), so that three signed int8 digits hold it, or in
                     // [2^7, 2^8), below the largest e4m3 value
-                    const int e = max(-120, min(120, (kInt ? 148 : 134) - static_cast<int>(__float_as_uint(amax) >> 23)));
+                    const int e = max(-120, min(120, (kInt ? 148 : 134) - static_cast<int>(amax >> 23)));
                     up[h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                     down[h] = R * it.rt + rr0 + h < it.s.rows
                                   ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
                                   : 0.0f;
+                    if (amax >= 0x7F800000u) down[h] = NAN;  // no digits hold such a row: all its scores are NaN
                 }
                 if (lane == 0) S.rowf[slot][rr0 / 4] = make_float4(down[0], down[1], down[2], down[3]);
 #pragma unroll
@@ -822,8 +870,9 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                                    to_u32_sat(u[2 * h + 1].y));
             }
             if constexpr (!kInt) {
-                // column of digit k of row r: R k + r
-#pragma unroll
+                // column of digit k of row r: R k + r.  (A loop of 16 rows' digits written out five times does not stay in the
+                // instruction cache beside the helpers' loops: 24 sequences of 80 heads on 8 148 us instead of 126)
+#pragma unroll(R == 8 ? Sh::kVD : 1)
                 for (int k = 0; k < Sh::kVD; ++k) {
                     uint32_t d[kRW / 4];
 #pragma unroll
@@ -925,6 +974,8 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                 if (flags & kBoth) ++handovers;
                 any_of<kGroup>(false, g);  // the sums have been read
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.info_empty[i % kInfo]);
         }
     }
     tc_fence_before_sync();

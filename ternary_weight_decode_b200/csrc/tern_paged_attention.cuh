@@ -93,11 +93,11 @@ __device__ __forceinline__ long long head_units(const AttnParams &p, const Seq &
     return u;
 }
 
-// 1 / x within a rounding error (x not subnormal), 0 for x = 0.
+// 1 / x within a rounding error (x not subnormal), 0 for x = 0, NaN for NaN.
 __device__ __forceinline__ float recip(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return x > 0.0f ? y : 0.0f;
+    return x == 0.0f ? 0.0f : y;
 }
 
 __device__ __forceinline__ float ex2(float x) {

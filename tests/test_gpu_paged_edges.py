@@ -83,6 +83,35 @@ def test_nan_codes_reach_only_the_rows_that_see_them(n, window):
         assert np.all(np.isnan(out[~others][:, 5]))
 
 
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+def test_queries_that_are_not_finite(n, value, kind):
+    """Their rows are NaN (0 where nothing is seen), the others what they are."""
+    rng = np.random.default_rng(n)
+    Hq, Hkv, page, ctx = 6, 2, 32, [n + 300, n - 1 if n > 1 else 40]
+    pages, n_pages = page_table(rng, ctx, page)
+    ref = mid_cache(rng, kind, Hkv, page, n_pages)
+    start = np.array([0, n, 2 * n])
+    q = rng.standard_normal((2 * n, Hq, D)).astype(np.float32)
+    want = paged.attention(q, start, ctx, pages, ref, kind)
+    k_ref, v_ref, _ = paged.values(np.array([0, ctx[0], sum(ctx)]), ctx, pages, ref, kind)
+    tol = bound(q, k_ref, v_ref, D ** -0.5, max(ctx))
+    bad = np.zeros((2 * n, Hq), bool)
+    bad[n - 1, 1] = bad[n, 4] = bad[2 * n - 1, 0] = True   # row n sees nothing when n > 1
+    q[bad, 77] = value
+    dev = device_cache(ref, kind)
+    out = torch.full((2 * n, Hq, D), -2.0, device="cuda")
+    tern.tern_attention_paged(to_dev(q), tern.PagedBatch(i32(start), i32(ctx), i32(pages), 2 * n, n, max(ctx)), dev, out,
+                              tern.attention_paged_workspace(Hq, dev))
+    out = out.cpu().numpy()
+    assert np.all(np.abs(out - want)[~bad] <= tol)
+    if n > 1:
+        assert np.all(out[n] == 0)
+        bad[n] = False
+    assert np.all(np.isnan(out[bad]))
+
+
 # ---------------------------------------------------------------- many sequences
 @pytest.mark.parametrize("kind", [INT8, E4M3])
 @pytest.mark.parametrize("B", [256, 257, 300, 1000])
