@@ -54,7 +54,7 @@
 // next item's digits while this one's tiles are worked off.
 //
 // Measured (device time; the floor is the codes at the measured copy rate): 24
-// sequences of 24000 to 40000 tokens, 40 heads on 8, 98 us of 86 (e4m3 and
+// sequences of up to 20011 tokens, 40 heads on 8, 98 us of 86 (e4m3 and
 // int8, 16-token pages); one of 65536 33.4 of 20.5, of 4096 12.9 of 1.3 (some 8
 // us are launch, look-up and the merging of divided items); 16 sequences of
 // which a window and sinks show 4100 tokens 34 of 20.7; three sequences of 16
