@@ -734,11 +734,10 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     for (int r = 0; r < 4; ++r) {
                         const uint32_t *d = sv + 2 * Sh::kQD * r;
                         float2 t;
-                        if constexpr (kInt) {  // ((d2 2^8) + d1) 2^8 + d0
-                            const float2 up = make_float2(256.0f, 256.0f);
-                            t = make_float2(small_int(d[4]), small_int(d[5]));
-                            t = __ffma2_rn(t, up, make_float2(small_int(d[2]), small_int(d[3])));
-                            t = __ffma2_rn(t, up, make_float2(small_int(d[0]), small_int(d[1])));
+                        if constexpr (kInt) {  // (d2 2^8 + d1) 2^8 + d0: the first sum is an integer below 2^30, rounded to fp32
+                            t = make_float2(static_cast<float>(static_cast<int>(256 * d[4] + d[2])),
+                                            static_cast<float>(static_cast<int>(256 * d[5] + d[3])));
+                            t = __ffma2_rn(t, make_float2(256.0f, 256.0f), make_float2(small_int(d[0]), small_int(d[1])));
                         } else {  // d0 + (d1 + ...) / 16
                             const float2 down = make_float2(0.0625f, 0.0625f);
                             t = make_float2(__uint_as_float(d[8]), __uint_as_float(d[9]));
