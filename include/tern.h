@@ -632,9 +632,15 @@ tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_ca
  *  tern_attention_paged_workspace_bytes() bytes, its first 4096 bytes all zero
  *  before its first use (counters, zero again after every call); calls that
  *  may overlap need separate ones.
- * Sums and softmax statistics are held in fp32, and the order of every sum is
- * fixed by the lengths: the same inputs give the same bits.  T = 0 does
- * nothing.  Errors: TERN_EINVAL for a bad batch or cache, bad shapes, strides,
+ * Sums and softmax statistics are held in fp32 (products and partial sums of
+ * int8 codes exactly in int32), and the order of every sum is fixed by the
+ * lengths: the same inputs give the same bits.  A query is held to 2^-24 of its
+ * row's largest element (int8) or 2^-20 of each element (e4m3), a softmax
+ * weight to 2^-26 of the largest or 2^-20 of itself.  A query row with a NaN or
+ * an infinity gives NaN, as does a NaN code (e4m3) for the rows that see its
+ * token; scales of visible blocks must be positive and finite, as the append
+ * writes them, and what lies behind a sequence's last token may hold anything.
+ * T = 0 does nothing.  Errors: TERN_EINVAL for a bad batch or cache, bad shapes, strides,
  * pointers or workspace, TERN_EUNSUPPORTED for D != 128, TERN_ECUDA.
  */
 tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const tern_paged_batch *batch,

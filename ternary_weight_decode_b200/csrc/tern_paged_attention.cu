@@ -54,12 +54,12 @@
 // next item's digits while this one's tiles are worked off.
 //
 // Measured (device time; the floor is the codes at the measured copy rate): 24
-// sequences of up to 20011 tokens, 40 heads on 8, 98 us of 86 (e4m3 and
-// int8, 16-token pages); one of 65536 33.4 of 20.5, of 4096 12.9 of 1.3 (some 8
-// us are launch, look-up and the merging of divided items); 16 sequences of
-// which a window and sinks show 4100 tokens 34 of 20.7; three sequences of 16
-// drafted tokens 56 of 8.0 and a prompt's 2048 rows of 4096 tokens 540 of 79:
-// there some 20 instructions an element of the softmax and the ends of items.
+// sequences of up to 20011 tokens, 40 heads on 8, 97 us of 86 (int8 101; 16-token
+// pages); one of 65536 32.5 of 20.5, of 4096 12.9 of 1.3 (some 8 us are launch,
+// look-up and the merging of divided items); 16 sequences of which a window and
+// sinks show 4100 tokens 34 of 20.7; three sequences of 16 drafted tokens 55 of
+// 8.0 and a prompt's 2048 rows of 4096 tokens 524 of 79: there some 20
+// instructions an element of the softmax, and the ends of items.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
