@@ -163,8 +163,7 @@ constexpr int kLineThreads = 256;
 struct LineShared {
     long long chunk[kLineThreads];  // line index where each thread's sequences begin
     long long scan[kLineThreads / 32];
-    Seq seq[kLineThreads];          // with one sequence a thread at most: the sequences,
-    int head[kLineThreads];         // and the tiles of one KV head of each
+    Seq seq[kLineThreads];          // with one sequence a thread at most: the sequences
 };
 struct Line {
     long long total;
@@ -192,21 +191,22 @@ __device__ __forceinline__ Line make_line(const AttnParams &p, LineShared &S) {
         for (int b = tid * L.per; b < min(v.B, tid * L.per + L.per); ++b)
             mine += v.Hkv * head_units<R>(p, sequence(p, b));
     } else if (counts && !many) {
-        S.head[tid] = static_cast<int>(head_units<R>(p, s));
+        S.chunk[tid] = head_units<R>(p, s);  // (for now: the tiles of one KV head)
     } else if (counts) {
 #pragma unroll 1
         for (int b = warp; b < v.B; b += kLineThreads / 32) {
             const Seq t = S.seq[b];
-            int n = 0;
+            long long n = 0;
 #pragma unroll 1
             for (int rt = lane; rt * R < t.rows; rt += 32) n += tile_count(tiles_of<R>(p, t, rt));
-            n = warp_sum_int(n);
-            if (lane == 0) S.head[b] = n;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            if (lane == 0) S.chunk[b] = n;
         }
     }
     __syncthreads();
     if (counts) {
-        if (L.per == 1 && tid < v.B) mine = static_cast<long long>(v.Hkv) * S.head[tid];
+        if (L.per == 1 && tid < v.B) mine = v.Hkv * S.chunk[tid];
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -245,13 +245,14 @@ __device__ __forceinline__ Cursor find_place(const AttnParams &p, const LineShar
 #pragma unroll 1
     for (;; ++b) {
         cur.s = seq_of(b);
-        ph = L.per == 1 ? S.head[b] : head_units<R>(p, cur.s);
+        ph = L.per == 1 ? quot((b + 1 < kLineThreads ? S.chunk[b + 1] : L.total) - S.chunk[b], p.v.Hkv)
+                        : head_units<R>(p, cur.s);
         if (off < ph * p.v.Hkv || b + 1 == p.v.B) break;  // (the second: lengths that changed under the kernel end here)
         off -= ph * p.v.Hkv;
     }
     cur.b = b;
     cur.head = min(static_cast<int>(quot(off, max(ph, 1LL))), p.v.Hkv - 1);
-    int k = static_cast<int>(off - cur.head * ph);
+    long long k = off - cur.head * ph;
     // the row tile, 32 at a time
 #pragma unroll 1
     for (int rt0 = 0;; rt0 += 32) {
@@ -266,7 +267,7 @@ __device__ __forceinline__ Cursor find_place(const AttnParams &p, const LineShar
         if (past || (rt0 + 32) * R >= cur.s.rows) {
             const int l = past ? __ffs(past) - 1 : 0;
             cur.rt = rt0 + l;
-            cur.k = k - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, n, l));
+            cur.k = static_cast<int>(k) - (__shfl_sync(0xffffffffu, incl, l) - __shfl_sync(0xffffffffu, n, l));
             break;
         }
         k -= __shfl_sync(0xffffffffu, incl, 31);

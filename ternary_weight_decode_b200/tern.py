@@ -563,25 +563,28 @@ def tern_attention_decode_q4_0(q: torch.Tensor, cache: KVCache, L: int, out: tor
 # ------------------------------------------------------------------ rotary embedding, paged KV cache
 # The calls below run once per layer and token, so they cost the host little:
 # the descriptors' structs are made and checked once (again when a field is
-# replaced), and each call checks its tensors with a few cheap queries.
+# replaced, or a tensor's memory or size), and each call checks its tensors with
+# a few cheap queries.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _Described:
-    """A descriptor whose C struct is kept until one of its fields is replaced."""
+    """A descriptor whose C struct is kept until a field is replaced, or one of
+    ``probes`` (where its tensors lie, and what may change in place) answers
+    otherwise."""
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         self.__dict__.pop("_kept", None)
 
     def described(self):
-        """(address of the struct, device index)"""
+        """(address of the struct, device index, the struct)"""
         kept = self.__dict__.get("_kept")
-        if kept is None:
-            s = self.struct()
-            kept = (ctypes.addressof(s), self.device_index(), s)
+        if kept is None or [f() for f in kept[1]] != kept[2]:
+            s, probes = self.struct(), self.probes()
+            kept = ((ctypes.addressof(s), self.device_index(), s), probes, [f() for f in probes])
             self.__dict__["_kept"] = kept
-        return kept
+        return kept[0]
 
 
 def _one_device(*tensors) -> int:
@@ -649,6 +652,11 @@ class RopePlan(_Described):
     def device_index(self) -> int:
         return _one_device(self.table)
 
+    def probes(self) -> tuple:
+        if self.sections is None:
+            return self.table.data_ptr, self.table.numel
+        return self.table.data_ptr, self.table.numel, lambda: tuple(self.sections)
+
     def struct(self) -> tern_rope_plan:
         t = self.table
         assert t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 3 and t.shape[2] == 2
@@ -703,6 +711,10 @@ class PagedCache(_Described):
     def device_index(self) -> int:
         return _one_device(self.k_codes, self.k_scales, self.v_codes, self.v_scales)
 
+    def probes(self) -> tuple:
+        return (self.k_codes.data_ptr, self.k_scales.data_ptr, self.v_codes.data_ptr, self.v_scales.data_ptr,
+                self.k_codes.numel)
+
     def struct(self) -> tern_paged_cache:
         n = self.k_codes.shape[0]
         for codes, scales in ((self.k_codes, self.k_scales), (self.v_codes, self.v_scales)):
@@ -727,6 +739,9 @@ class PagedBatch(_Described):
 
     def device_index(self) -> int:
         return _one_device(self.row_start, self.ctx, self.pages)
+
+    def probes(self) -> tuple:
+        return (self.row_start.data_ptr, self.ctx.data_ptr, self.pages.data_ptr, self.ctx.numel, self.pages.numel)
 
     def struct(self) -> tern_paged_batch:
         B = self.ctx.shape[0]

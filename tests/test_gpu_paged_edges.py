@@ -221,6 +221,45 @@ def test_sequences_that_share_pages():
     close(out, q, start, ctx, pages, ref, INT8)
 
 
+def test_descriptors_follow_their_tensors():
+    """A tensor whose memory or size changes in place, or a field replaced, is seen by the next call."""
+    rng = np.random.default_rng(42)
+    Hq, Hkv, page = 4, 2, 16
+    pages = np.array([[0, 1, 2], [3, 4, 5]], np.int32)
+    ref = mid_cache(rng, INT8, Hkv, page, 6)
+    dev = device_cache(ref, INT8)
+    ws = tern.attention_paged_workspace(Hq, dev)
+    q = rng.standard_normal((2, Hq, D)).astype(np.float32)
+    batch = tern.PagedBatch(i32([0, 1, 2]), i32([20, 30]), i32(pages), 2, 1, 48)
+
+    def check(n, ctx):
+        out = torch.full((n, Hq, D), -2.0, device="cuda")
+        tern.tern_attention_paged(to_dev(q[:n]), batch, dev, out, ws)
+        close(out, q[:n], np.arange(n + 1), ctx, pages, ref, INT8)
+    check(2, [20, 30])
+    batch.ctx.set_(i32([48, 3]))
+    check(2, [48, 3])
+    other = mid_cache(rng, INT8, Hkv, page, 6)
+    for x in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        getattr(dev, x).data = to_dev(other[x])
+    ref = other
+    check(2, [48, 3])
+    batch.ctx.resize_(1)
+    batch.row_start.resize_(2)
+    batch.pages.resize_(1, 3)
+    batch.T = 1
+    check(1, [48])
+
+    table = paged.rope_table(10000.0, D, 40)
+    plan = tern.RopePlan(to_dev(table), [10, 54])
+    pos = np.array([[3, 9], [30, 1]], np.int32)
+    for sections in ([10, 54], [60, 4]):
+        plan.sections[:] = sections
+        y = torch.empty(2, Hq, D, device="cuda")
+        tern.tern_rope(plan, to_dev(pos), to_dev(q), y)
+        np.testing.assert_array_equal(y.cpu().numpy(), paged.rope(q, pos, table, sections)[0])
+
+
 # ---------------------------------------------------------------- streams, graphs, workspaces
 class Call:
     def __init__(self, seed, n, ctx, kind, Hq, Hkv, page=32, window=0):
