@@ -5,8 +5,8 @@
 //    each: the two halves' float4, or two adjacent float4 when pairs are
 //    interleaved), so rows may be rotated in place and a row's cosines are read
 //    once per thread.
-//  * append_paged_kernel: the first CTAs rotate the queries the same way; the
-//    others take the new blocks of the cache, four warps per (block of 16
+//  * append_paged_kernel: some CTAs rotate the queries the same way; the others
+//    take the new blocks of the cache, four warps per (block of 16
 //    tokens, KV head, K or V): half a warp per token, eight elements a lane, all
 //    of the block's new tokens in registers, so each input is read once and the
 //    block's maximum is a warp reduction and four words of shared memory.
@@ -264,7 +264,9 @@ struct AppendParams {
     float *q_out;
     int ldqo;
     int32_t *d_invalid;
-    int q_ctas;      // CTAs that rotate queries
+    int kv_ctas;     // CTAs of the cache: every `every`-th of the first every * kv_ctas; the others rotate queries
+    int every;
+    FastDiv by_every;
     RowShare share;
     int group;       // rows of a KV CTA
 };
@@ -397,10 +399,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_paged_kernel(AppendP
     const PagedView &v = p.v;
     const int tid = threadIdx.x, lane = tid & 31;
     pdl_wait();
-    if (static_cast<int>(blockIdx.x) < p.q_ctas) {
+    const int kv = min(p.by_every.quot(blockIdx.x), p.kv_ctas), in = static_cast<int>(blockIdx.x) - kv * p.every;
+    if (kv == p.kv_ctas || in != 0) {
         const int q = tid >> 4, j = tid & 15;
         const int rl = p.share.slots.quot(q), slot = q - rl * p.share.hs;
-        const int64_t t = static_cast<int64_t>(blockIdx.x) * p.share.rows + rl;
+        const int64_t t = (static_cast<int64_t>(kv) * (p.every - 1) + (kv == p.kv_ctas ? in : in - 1)) * p.share.rows + rl;
         if (rl < p.share.rows && t < v.T)
             rotate_row(p.R, p.pos, v.T, p.axes, static_cast<int>(t), j, slot, p.share.hs, p.Hq, kPD, p.q + t * p.ldq,
                        p.q_out + t * p.ldqo, nullptr, v.row_start, v.row_start + v.B);
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_paged_kernel(AppendP
     }
     for (int i = tid; i <= v.B; i += kAppendThreads) starts[i] = v.row_start[i];
     __syncthreads();
-    const int64_t u = blockIdx.x - p.q_ctas;
+    const int64_t u = kv;
     // a CTA per (p.group rows, KV head), four warps for K and four for V; each row that is the first of a block is one
     // block's work
     const int64_t rg = u / v.Hkv, t0 = rg * p.group;
@@ -505,13 +508,16 @@ cudaError_t launch_kv_append_paged(const AppendLaunch &A, cudaStream_t s) {
     p.d_invalid = A.d_invalid;
     const int64_t T = A.batch.T;
     p.share = row_share(A.Hq, 16);
-    p.q_ctas = static_cast<int>(blocks_of(T, p.share.rows));
     // a CTA per 16 rows and KV head, but per row where sequences have few (there nearly every row is the first of its
     // block, and 16 of them one after another took longer).  251 rows of one sequence: 5.6 us per 16, 7.3 us per row.
     p.group = A.batch.max_rows >= kPB ? kPB : 1;
-    const int64_t kv_ctas = ceil_div(T, p.group) * A.cache.Hkv;
+    const int64_t kv_ctas = ceil_div(T, p.group) * A.cache.Hkv, ctas = blocks_of(T, p.share.rows) + kv_ctas;
+    // the cache's CTAs, whose time is latency, spread among those of the queries, whose time is memory's
+    p.kv_ctas = static_cast<int>(kv_ctas);
+    p.every = static_cast<int>(std::max<int64_t>(1, ctas / kv_ctas));
+    p.by_every = fast_div(p.every);
     return launch_pdl(A.cache.kind == TERN_KV_INT8 ? append_paged_kernel<TERN_KV_INT8> : append_paged_kernel<TERN_KV_E4M3>,
-                      dim3(static_cast<unsigned>(p.q_ctas + kv_ctas)), kAppendThreads,
+                      dim3(static_cast<unsigned>(ctas)), kAppendThreads,
                       static_cast<size_t>(A.batch.B + 1) * sizeof(int32_t), s, p);
 }
 
