@@ -21,7 +21,8 @@
 // Measured (device time, and the bytes at the measured copy rate): rotation of
 // 2048 rows of 48 heads 19.9 us (15.5), of 777 rows of 32 heads, 64 of 128
 // elements, 8.5 (3.9); append and read back of 4096 rows of 40 + 2 x 8 heads
-// 47.0 + 11.6 (38.7), of 33 ragged sequences of up to 16 rows 9.5 + 3.0 (2.8),
+// 41.1 + 11.6 (38.7; the cache's CTAs behind the queries' instead of among
+// them 47.0), of 33 ragged sequences of up to 16 rows 9.5 + 3.0 (2.8),
 // of one row 3.4 + 2.1.
 #include <algorithm>
 
