@@ -565,7 +565,7 @@ def tern_attention_decode_q4_0(q: torch.Tensor, cache: KVCache, L: int, out: tor
 # the descriptors' structs are made and checked once (again when a field is
 # replaced, or a tensor's memory or size), and each call checks its tensors with
 # a few cheap queries.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class _Described:
@@ -596,7 +596,7 @@ def _one_device(*tensors) -> int:
 
 def _call_stream(dev: int, stream) -> int:
     """The raw stream of a call on device `dev`, which has to be the current one."""
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     if dev != cur:
         raise ValueError(f"the buffers are on cuda:{dev}, the current device is cuda:{cur}")
     return _raw_stream(cur) if stream is None else stream.cuda_stream
@@ -606,10 +606,10 @@ def _heads(t: torch.Tensor, dev: int, T: int, H: int, D: int) -> int:
     """The row stride of fp32 rows of heads, a tensor or view [T, H, D] on device `dev`."""
     if t.get_device() != dev:
         raise ValueError(f"a buffer is on {t.device}, the others are on cuda:{dev}")
-    assert t.dtype == torch.float32 and t.shape == (T, H, D), (t.dtype, tuple(t.shape), (T, H, D))
-    st = t.stride()
-    assert st[2] == 1 and (st[1] == D or H == 1), "the heads of a row must be contiguous"
-    return st[0] if T > 1 else H * D
+    assert t.dtype is torch.float32 and t.shape == (T, H, D), (t.dtype, tuple(t.shape), (T, H, D))
+    s0, s1, s2 = t.stride()
+    assert s2 == 1 and (s1 == D or H == 1), "the heads of a row must be contiguous"
+    return s0 if T > 1 else H * D
 
 
 def _positions(t: torch.Tensor, dev: int, axes: int, T: int) -> int:
