@@ -260,6 +260,14 @@ def test_descriptors_follow_their_tensors():
         np.testing.assert_array_equal(y.cpu().numpy(), paged.rope(q, pos, table, sections)[0])
 
 
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("n,ctx,Hq,Hkv,page,window", [([1, 3], [700, 5], 71, 1, 4096, 0), ([2], [260], 128, 1, 112, 33),
+                                                      ([37], [4200], 3, 3, 4096, 0), ([1], [1030], 64, 64, 16, 0)])
+def test_large_groups_and_pages(n, ctx, Hq, Hkv, page, window, kind):
+    """Many query heads on one KV head, many KV heads, the largest page, and one no power of two divides."""
+    attend(np.random.default_rng(Hq), n, ctx, page, kind, Hq, Hkv, window=window, sinks=2)
+
+
 # ---------------------------------------------------------------- streams, graphs, workspaces
 class Call:
     def __init__(self, seed, n, ctx, kind, Hq, Hkv, page=32, window=0):
