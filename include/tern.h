@@ -650,6 +650,19 @@ tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const 
                                  float *out, int32_t ldo, void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * Test hook of the paged attention's copies (no counterpart on the pages):
+ * how a tile of eight 16-token blocks of K or V is divided into copies, by the
+ * functions that the kernel calls.  Runs on the host; at and size are host
+ * memory.
+ *  at[8]: the place of each block in the cache, in blocks of one head, -1 for
+ *  a missing one.
+ *  size[8]: log2 of the blocks (1, 2, 4 or 8) that the copy beginning at each
+ *  block takes, -1 where none begins.
+ * Errors: TERN_EINVAL for a null pointer.
+ */
+tern_status tern_debug_paged_copies(const int32_t *at, int32_t *size);
+
+/*
  * Test hook of the streamed kernels (the integer dot product and the
  * in-kernel quantisation of the Bonsai page, "Decode 为什么只能算一般"): runs
  * tern_gemv_streamed (W1 == NULL, no residual) or tern_gateup_swiglu_streamed

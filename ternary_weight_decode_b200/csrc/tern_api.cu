@@ -383,6 +383,12 @@ tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const 
     return cuda_status(e, name);
 }
 
+tern_status tern_debug_paged_copies(const int32_t *at, int32_t *size) {
+    if (!at || !size) return fail(TERN_EINVAL, "%s: at and size are required", "tern_debug_paged_copies");
+    tern::paged_copies(at, size);
+    return TERN_OK;
+}
+
 tern_status act_quant_fwht(const void *x, int32_t x_is_fp16, int32_t M, int32_t K, int32_t ldx,
                            int32_t fwht_block, int32_t flags, int8_t *q, int32_t ldq, float *s_x,
                            void *stream) {

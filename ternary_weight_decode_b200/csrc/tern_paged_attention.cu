@@ -401,12 +401,8 @@ __device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &ma
             // runs of blocks that lie behind one another in the cache: one copy each for 8, 4, 2 or 1 of them
             // (copies of 16 rows: 2150 cycles a tile, of 64 rows 1690)
             const int before = __shfl_up_sync(0xffffffffu, bi, 1);
-            const unsigned follows = __ballot_sync(0xffffffffu, bi >= 0 && bi == before + 1) >> (8 * sub);
-            int size = 0;  // log2 of the blocks that this block's copy takes, -1: another's does
-            if ((follows & 0xFEu) == 0xFEu) size = 3;
-            else if ((follows >> (j & 4) & 0xEu) == 0xEu) size = 2;
-            else if (follows >> (j & 6) & 2u) size = 1;
-            if (bi < 0 || (j & ((1 << size) - 1))) size = -1;
+            const unsigned follows = __ballot_sync(0xffffffffu, continues_block(before, bi)) >> (8 * sub) & 255;
+            const int size = copy_size(follows, j, bi);
             // masks: a block whose tokens not every row sees, or that is missing
             const int p_min = it.s.first + p.by_gq.quot(R * it.rt);
             const int p_max = it.s.first + p.by_gq.quot(min(R * it.rt + R, it.s.rows) - 1);
@@ -1000,6 +996,12 @@ cudaError_t launch_rows(const AttnParams &p, const CacheMaps &maps, int ctas, cu
 }
 
 }  // namespace
+
+void paged_copies(const int32_t *at, int32_t *size) {
+    unsigned follows = 0;
+    for (int j = 1; j < kTB; ++j) follows |= continues_block(at[j - 1], at[j]) ? 1u << j : 0u;
+    for (int j = 0; j < kTB; ++j) size[j] = copy_size(follows, j, at[j]);
+}
 
 size_t attention_paged_workspace_bytes(int num_sms) {
     // the counters, and two partial records a CTA (one CTA per SM)

@@ -17,6 +17,22 @@ namespace tern {
 constexpr int kTB = 8;           // blocks of a tile
 constexpr int kMaxRows = 32;     // rows of an item, at most
 constexpr int kMaxCtas = 1024;   // CTAs of a launch (counters at the workspace's start)
+
+// The copies of a tile: block j of the tile lies at place at[j] of the cache
+// (in blocks of one head), -1 when it is missing.  Blocks that lie behind one
+// another there are copied together, 8, 4, 2 or 1 at a time, each copy at a
+// place of the tile that its size divides.
+// Whether block j continues block j - 1 (a missing block is continued by none,
+// not even by place 0, which is one above its -1).
+__host__ __device__ constexpr bool continues_block(int before, int at) { return before >= 0 && at == before + 1; }
+// log2 of the blocks that the copy beginning at block j takes, -1 when none
+// begins there (the block is missing, or another's copy takes it).  follows:
+// bit i when block i continues block i - 1.
+__host__ __device__ constexpr int copy_size(unsigned follows, int j, int at) {
+    const int size = (follows & 0xFEu) == 0xFEu ? 3 : (follows >> (j & 4) & 0xEu) == 0xEu ? 2 : follows >> (j & 6) & 2u ? 1 : 0;
+    return at < 0 || (j & ((1 << size) - 1)) ? -1 : size;
+}
+
 // A partial record: [rows][kPD] sums, then (m, z) of each row.
 __host__ __device__ constexpr int rec_floats(int rows) { return rows * (kPD + 2); }
 

@@ -163,6 +163,7 @@ def lib() -> ctypes.CDLL:
                 "tern_attention_paged_workspace_bytes": (ctypes.c_int, [i32, p, ctypes.POINTER(sz)]),
                 "tern_attention_paged": (ctypes.c_int, [p, i32, i32, p, p, i32, i32, ctypes.c_float, p, i32, p,
                                                         sz, p]),
+                "tern_debug_paged_copies": (ctypes.c_int, [p, p]),
                 "tern_gemv_fused": (ctypes.c_int, [pm, p, i32, p, i32, i32, i32, p, p, i32, p, i32, p]),
                 "tern_gateup_swiglu_fused": (ctypes.c_int, [pm, pm, p, i32, p, i32, i32, i32, p, i32,
                                                             p, i32, p]),
@@ -820,6 +821,15 @@ def tern_attention_paged(q: torch.Tensor, batch: PagedBatch, cache: PagedCache, 
         _call_stream(dev, stream))
     if st:
         _check(st, "tern_attention_paged")
+
+
+def tern_debug_paged_copies(at) -> list[int]:
+    """log2 of the blocks that the copy beginning at each of a tile's eight blocks takes, -1 where
+    none begins; at: the blocks' places in the cache, -1 for a missing one."""
+    assert len(at) == 8
+    size = (ctypes.c_int32 * 8)()
+    _check(lib().tern_debug_paged_copies((ctypes.c_int32 * 8)(*at), size), "tern_debug_paged_copies")
+    return list(size)
 
 
 ENGINE_TENSOR_CORES, ENGINE_CUDA_CORES = 0, 1
