@@ -663,6 +663,18 @@ tern_status tern_attention_paged(const float *q, int32_t ldq, int32_t Hq, const 
 tern_status tern_debug_paged_copies(const int32_t *at, int32_t *size);
 
 /*
+ * Test hook of the paged attention's waits (no counterpart on the pages): the
+ * SM cycles after which a wait of later tern_attention_paged calls on the
+ * current device gives up, 1 .. 1e9; 0 restores the usual 1e9.  With a budget
+ * shorter than ordinary waits take, a call records the device error
+ * (tern_device_error) and ends; its rows of out may hold anything, nothing
+ * else is written, and its workspace has to be zeroed before its next use.
+ * Not to be changed while such a call runs.  Errors: TERN_EINVAL for a budget
+ * out of range, TERN_ECUDA.
+ */
+tern_status tern_debug_paged_wait_budget(int64_t cycles);
+
+/*
  * Test hook of the streamed kernels (the integer dot product and the
  * in-kernel quantisation of the Bonsai page, "Decode 为什么只能算一般"): runs
  * tern_gemv_streamed (W1 == NULL, no residual) or tern_gateup_swiglu_streamed
@@ -733,8 +745,8 @@ tern_status tern_debug_select_engine(int32_t engine);
  * bounded wait in a kernel ran out since the last call, else a nonzero code
  * (1: a wait on an mbarrier, a cluster peer or a neighbour's partial ran
  * out).  Synchronises `stream`.  Library plumbing (no counterpart on the
- * pages).  After a nonzero code, zero every streamed workspace the failed
- * calls used before using it again.
+ * pages).  After a nonzero code, zero every workspace of a streamed or paged
+ * attention call that failed before using it again.
  */
 tern_status tern_device_error(int32_t *code_out, void *stream);
 

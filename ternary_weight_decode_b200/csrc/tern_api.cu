@@ -389,6 +389,13 @@ tern_status tern_debug_paged_copies(const int32_t *at, int32_t *size) {
     return TERN_OK;
 }
 
+tern_status tern_debug_paged_wait_budget(int64_t cycles) {
+    const char *name = "tern_debug_paged_wait_budget";
+    if (cycles < 0 || cycles > tern::kWaitBudgetCycles)
+        return fail(TERN_EINVAL, "%s: cycles must be 0 (the usual budget) or 1 .. 1e9", name);
+    return cuda_status(tern::set_paged_wait_budget(cycles == 0 ? tern::kWaitBudgetCycles : cycles), name);
+}
+
 tern_status act_quant_fwht(const void *x, int32_t x_is_fp16, int32_t M, int32_t K, int32_t ldx,
                            int32_t fwht_block, int32_t flags, int8_t *q, int32_t ldq, float *s_x,
                            void *stream) {

@@ -133,6 +133,7 @@ struct PagedAttentionLaunch {
     int num_sms;
 };
 size_t attention_paged_workspace_bytes(int num_sms);
+cudaError_t set_paged_wait_budget(long long cycles);
 void paged_copies(const int32_t *at, int32_t *size);  // (host)
 cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s, const char **why);
 

@@ -197,11 +197,24 @@ __device__ __forceinline__ uint32_t e4m3_digit(float2 &x) {
     return d;
 }
 
-// A wait of this thread; once one has run out, none of the later ones waits.
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+// Waits.  One that runs out records the device error, and its thread waits no
+// more.  What a wait would have handed over (a tile's info, an item, a product)
+// is then not used for an address, a copy or a product: each warp of one role,
+// and each softmax group as a whole, leaves its loop, and waits once more for
+// the copies or products that it has in flight.  Those that wait for it run out
+// in turn, so the CTA ends, its tensor memory is given back, and its rows may
+// hold anything.
+__device__ long long g_wait_budget = kWaitBudgetCycles;  // (a test shortens it)
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, *const_cast<volatile long long *>(&g_wait_budget));
+}
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
     if (ok && !mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity);
 }
+// The wait for what a warp has in flight, which needs no other warp to end.
+__device__ __noinline__ bool land(uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+// Whether no lane's wait has run out (warp-collective).
+__device__ __forceinline__ bool all_ok(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 // An int32 of at most 22 bits as fp32, exactly, without the conversion unit.
 __device__ __forceinline__ float small_int(uint32_t c) {
@@ -291,56 +304,48 @@ __device__ __forceinline__ void add_sums(uint32_t taddr, float vref, float (&o)[
     }
 }
 
-// Copies of tile i's keys, values or both, by its info; lanes 0-7 a block each.
-template <int R, int KIND, bool K, bool V>
-__device__ __forceinline__ void copy_tile(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *kring, uint8_t *vring, int i,
-                                          bool &ok) {
-    const int lane = threadIdx.x & 31, at = lane * kPB * kPD;
-    const int ik = i % Shape<R, KIND>::kStages, iv = i % Shape<R, KIND>::kVStages;
+// Copies of tile i's keys, or values, by its info; lanes 0-7 a block each.
+// False when a wait ran out, here or before: nothing is copied.
+template <int R, int KIND, bool K>
+__device__ __forceinline__ bool copy_tile(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *ring, int i, bool &ok) {
+    constexpr int kSt = K ? Shape<R, KIND>::kStages : Shape<R, KIND>::kVStages;
+    const int lane = threadIdx.x & 31, stage = i % kSt;
+    uint64_t *full = K ? &S.k_full[stage] : &S.v_full[stage];
     const TileInfo &f = S.info[i % kInfo];
     const int size = lane < kTB ? f.size[lane] : -1, row = lane < kTB ? f.row[lane] : 0;
     const uint32_t bytes = __popc(f.valid) * kPB * kPD;
-    if (K) {
-        wait(&S.k_empty[ik], ((i / Shape<R, KIND>::kStages) + 1) & 1, ok);
-        if (lane == 0) mbar_arrive_expect_tx(&S.k_full[ik], bytes);
-        __syncwarp();
-        if (size >= 0) tma_load_2d_nohint(kring + ik * kTileBytes + at, &maps.k[size], 0, row, &S.k_full[ik]);
+    wait(K ? &S.k_empty[stage] : &S.v_empty[stage], ((i / kSt) + 1) & 1, ok);
+    if (!all_ok(ok)) return false;
+    if (lane == 0) {
+        mbar_arrive_expect_tx(full, bytes);
+        if (!K) mbar_arrive(&S.info_empty[i % kInfo]);  // (the softmax is done with a tile only after K's copy)
     }
-    if (V) {
-        wait(&S.v_empty[iv], ((i / Shape<R, KIND>::kVStages) + 1) & 1, ok);
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&S.v_full[iv], bytes);
-            mbar_arrive(&S.info_empty[i % kInfo]);  // (the softmax is done with a tile only after K's copy)
-        }
-        __syncwarp();
-        if (size >= 0) tma_load_2d_nohint(vring + iv * kTileBytes + at, &maps.v[size], 0, row, &S.v_full[iv]);
-    }
+    __syncwarp();
+    if (size >= 0)
+        tma_load_2d_nohint(ring + stage * kTileBytes + lane * kPB * kPD, K ? &maps.k[size] : &maps.v[size], 0, row, full);
+    return true;
 }
 
-// Before a CTA that copies ends: no copy is in flight, even after a wait that ran out.
-template <int R, int KIND, bool K, bool V>
-__device__ __forceinline__ void copies_land(AttnShared<R, KIND> &S, int count) {
-    constexpr int kSt = Shape<R, KIND>::kStages, kVSt = Shape<R, KIND>::kVStages;
-    bool land = true;
-    if (K)
+// Before a warp that copied n tiles ends: none of its copies is in flight.
+template <int R, int KIND, bool K>
+__device__ __forceinline__ void copies_land(AttnShared<R, KIND> &S, int n) {
+    constexpr int kSt = K ? Shape<R, KIND>::kStages : Shape<R, KIND>::kVStages;
 #pragma unroll 1
-        for (int i = max(0, count - kSt); i < count; ++i) wait(&S.k_full[i % kSt], (i / kSt) & 1, land);
-    if (V)
-#pragma unroll 1
-        for (int i = max(0, count - kVSt); i < count; ++i) wait(&S.v_full[i % kVSt], (i / kVSt) & 1, land);
+    for (int i = max(0, n - kSt); i < n; ++i)
+        if (!land(K ? &S.k_full[i % kSt] : &S.v_full[i % kSt], (i / kSt) & 1)) break;
 }
 
 // All copies of K, or of V.
 template <int R, int KIND, bool K>
-__device__ __forceinline__ void copy_codes(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *kring, uint8_t *vring,
-                                           int count) {
+__device__ __forceinline__ void copy_codes(const CacheMaps &maps, AttnShared<R, KIND> &S, uint8_t *ring, int count) {
     bool ok = true;
+    int n = 0;
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-        wait(&S.info_full[i % kInfo], (i / kInfo) & 1, ok);
-        copy_tile<R, KIND, K, !K>(maps, S, kring, vring, i, ok);
+    for (; n < count; ++n) {
+        wait(&S.info_full[n % kInfo], (n / kInfo) & 1, ok);
+        if (!copy_tile<R, KIND, K>(maps, S, ring, n, ok)) break;
     }
-    copies_land<R, KIND, K, !K>(S, count);
+    copies_land<R, KIND, K>(S, n);
 }
 
 // Look-up of a range's tiles: writes the infos of the items and tiles.  Four
@@ -359,9 +364,11 @@ __device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &ma
     const int k_first = cur.k;
     if (lane == 0) S.first_item = {cur.head, cur.rt, cur.units(), cur.s};
     int step = sub, page = -1, in_page = 0, j0 = 0;
+    int nk = 0, nv = 0;  // tiles whose K, V are copied here
     float ks = 0.0f, vs = 0.0f;
+    int i0 = 0;
 #pragma unroll 1
-    for (int i0 = 0; i0 < count + 8; i0 += 4) {
+    for (; i0 < count + 8; i0 += 4) {
         const Cursor it = cur;
         const int page_now = page, in_page_now = in_page, j0_now = j0;
         const float ks_now = ks, vs_now = vs;
@@ -373,11 +380,13 @@ __device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &ma
             if (j == 0 && (cur.k == 0 || i0 + sub == 0)) {
                 const int slot = cur.ord % kItems;
                 wait(&S.item_empty[slot], ((cur.ord / kItems) + 1) & 1, ok);
-                S.item[slot].head = cur.head;
-                S.item[slot].rt = cur.rt;
-                S.item[slot].tiles = min(cur.units() - cur.k, count - i0 - sub);
-                S.item[slot].s = cur.s;
-                mbar_arrive(&S.item_full[slot]);
+                if (ok) {
+                    S.item[slot].head = cur.head;
+                    S.item[slot].rt = cur.rt;
+                    S.item[slot].tiles = min(cur.units() - cur.k, count - i0 - sub);
+                    S.item[slot].s = cur.s;
+                    mbar_arrive(&S.item_full[slot]);
+                }
             }
             const int kb = kTB * cur.k + j;
             if (kb < cur.tl.n) {
@@ -409,9 +418,10 @@ __device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &ma
             const bool whole = bi >= 0 && j0_now + kPB - 1 <= p_min &&
                                (p.window == 0 || j0_now > p_max - p.window || j0_now + kPB <= p.sinks);
             const unsigned not_whole = __ballot_sync(0xffffffffu, !whole) >> (8 * sub) & 255;
+            if (i < count) wait(&S.info_empty[i % kInfo], ((i / kInfo) + 1) & 1, ok);
+            if (!all_ok(ok)) break;
             if (i < count) {
                 TileInfo &f = S.info[i % kInfo];
-                wait(&S.info_empty[i % kInfo], ((i / kInfo) + 1) & 1, ok);
                 f.j0[j] = j0_now;
                 f.row[j] = bi * kPB;
                 f.size[j] = size;
@@ -448,7 +458,13 @@ __device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &ma
             if (j == 0 && i < count) mbar_arrive(&S.scales_full[i % kInfo]);
             if constexpr (!Shape<R, KIND>::kCopyWarps) {
 #pragma unroll 1
-                for (int e = i0 - 8; e < min(i0 - 4, count); ++e) copy_tile<R, KIND, true, true>(maps, S, kring, vring, e, ok);
+                for (int e = i0 - 8; e < min(i0 - 4, count); ++e) {
+                    if (!copy_tile<R, KIND, true>(maps, S, kring, e, ok)) break;
+                    ++nk;
+                    if (!copy_tile<R, KIND, false>(maps, S, vring, e, ok)) break;
+                    ++nv;
+                }
+                ok = all_ok(ok);  // (then the next step's vote ends the loop)
             }
         }
     }
@@ -458,9 +474,12 @@ __device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &ma
         note_cut(S.cut[0], ranges, it.head, it.rt, it.s, u0 - k_first, it.tiles);
     }
     // (the last tile's item, as the lane that looked it up has it: cut if it goes on and began in this range)
-    if (j == 0 && sub == (count - 1) % 4 && cur.k + 1 < cur.units() && cur.k <= count - 1)
+    if (i0 >= count + 8 && j == 0 && sub == (count - 1) % 4 && cur.k + 1 < cur.units() && cur.k <= count - 1)
         note_cut(S.cut[1], ranges, cur.head, cur.rt, cur.s, u0 + count - 1 - cur.k, cur.units());
-    if constexpr (!Shape<R, KIND>::kCopyWarps) copies_land<R, KIND, true, true>(S, count);
+    if constexpr (!Shape<R, KIND>::kCopyWarps) {
+        copies_land<R, KIND, true>(S, nk);
+        copies_land<R, KIND, false>(S, nv);
+    }
 }
 
 template <int KIND>
@@ -548,25 +567,27 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
         look_up<R, KIND>(p, maps, S, kring, vring, L, ranges, u0, count,
                          [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); });
     } else if (warp == Sh::kWarpK) {
-        copy_codes<R, KIND, true>(maps, S, kring, vring, count);
+        copy_codes<R, KIND, true>(maps, S, kring, count);
     } else if (warp == Sh::kWarpV) {
-        copy_codes<R, KIND, false>(maps, S, kring, vring, count);
+        copy_codes<R, KIND, false>(maps, S, vring, count);
     } else if (warp == Sh::kWarpQK) {
         // ---- S of each tile, as soon as its keys are there and its accumulator has been read
         if (lane == 0) {
             constexpr uint32_t id_s = kInt ? idesc_i8(128, Sh::kNS, 1, 1) : idesc_e4m3(128, Sh::kNS);
-            int item = -1;
+            int item = -1, i = 0, asked = -1;  // asked: the last item whose last tile was issued
 #pragma unroll 1
-            for (int i = 0; i < count; ++i) {
+            for (; i < count; ++i) {
                 const int stage = i % kSt, buf = i % Sh::kSBufs;
                 wait(&S.k_full[stage], (i / kSt) & 1, ok);
                 wait(&S.scales_full[i % kInfo], (i / kInfo) & 1, ok);
+                if (!ok) break;
                 const int flags = S.info[i % kInfo].flags;
                 if (flags & kFirst) {
                     ++item;
                     wait(&S.q_full[item & 1], (item >> 1) & 1, ok);
                 }
                 wait(&S.s_empty[buf], ((i / Sh::kSBufs) + 1) & 1, ok);
+                if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t a = smem_u32(kring + stage * kTileBytes), b = smem_u32(qbuf + (item & 1) * Sh::kQBytes);
 #pragma unroll
@@ -574,8 +595,16 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     mma_ss<KIND>(tmem + buf * Sh::kNS, smem_desc_sw128(a + 32 * k), smem_desc_sw128(b + 32 * k), id_s, k > 0);
                 tc_commit(&S.s_full[buf]);
                 tc_commit(&S.k_empty[stage]);
-                if (flags & kLast) tc_commit(&S.q_empty[item & 1]);
+                if (flags & kLast) {
+                    tc_commit(&S.q_empty[item & 1]);
+                    asked = item;
+                }
                 mbar_arrive(&S.s_full[buf]);  // (hands on the tile's info and the rows' scales, which this thread has acquired)
+            }
+            if (i < count && i > 0) {  // (each arrival that these products make)
+                land(&S.s_full[(i - 1) % Sh::kSBufs], ((i - 1) / Sh::kSBufs) & 1);
+                land(&S.k_empty[(i - 1) % kSt], ((i - 1) / kSt) & 1);
+                if (asked >= 0) land(&S.q_empty[asked & 1], (asked >> 1) & 1);
             }
         }
         __syncwarp();
@@ -584,11 +613,13 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
         if (lane == 0) {
             constexpr uint32_t id_o = (kInt ? idesc_i8(128, Sh::kNP, 1, 0) : idesc_e4m3(128, Sh::kNP)) | (1u << 15) |
                                       (1u << 16);  // both operands M/N-major
+            int i = 0;
 #pragma unroll 1
-            for (int i = 0; i < count; ++i) {
+            for (; i < count; ++i) {
                 const int stage = i % Sh::kVStages, g = i & 1;
                 wait(&S.v_full[stage], (i / Sh::kVStages) & 1, ok);
                 wait(&S.p_full[g], (i >> 1) & 1, ok);
+                if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t a = smem_u32(vring + stage * kTileBytes), b = smem_u32(pbuf + g * Sh::kPBytes);
                 const uint32_t acc = S.accumulate[g];
@@ -599,6 +630,10 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                 tc_commit(&S.p_empty[g]);
                 tc_commit(&S.v_empty[stage]);
             }
+            if (i < count && i > 0) {
+                land(&S.p_empty[(i - 1) & 1], ((i - 1) >> 1) & 1);
+                land(&S.v_empty[(i - 1) % Sh::kVStages], ((i - 1) / Sh::kVStages) & 1);
+            }
         }
         __syncwarp();
     } else if (warp == Sh::kWarpQ) {
@@ -607,8 +642,9 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
         for (int done = 0, item = 0; done < count; ++item) {
             const int slot = item % kItems;
             wait(&S.item_full[slot], (item / kItems) & 1, ok);
-            const ItemInfo it = S.item[slot];
             wait(&S.q_empty[item & 1], ((item >> 1) + 1) & 1, ok);
+            if (!all_ok(ok)) break;
+            const ItemInfo it = S.item[slot];
             uint8_t *qb = qbuf + (item & 1) * Sh::kQBytes;
 #pragma unroll 1
             for (int rr0 = 0; rr0 < R; rr0 += 4) {
@@ -709,7 +745,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     reinterpret_cast<float *>(S.m[g])[gt] = -INFINITY;
                     reinterpret_cast<float *>(S.mref[g])[gt] = 0.0f;
                 }
-                any_of<kGroup>(false, g);
+                // (no barrier: whatever the others find in m, they take new references below)
             }
             // scores of this token, in log2
             float x[kRW];
@@ -723,7 +759,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     for (int e = 0; e < Sh::kQD; ++e)
                         tmem_ld8(ts + buf * Sh::kNS + 8 * Sh::kQD * h + 8 * e, *reinterpret_cast<uint32_t(*)[8]>(sv + 8 * e));
                     tmem_wait_ld();
-                    const float4 ra = S.rowf[f.ord % kItems][r0 / 4 + 2 * h], rb = S.rowf[f.ord % kItems][r0 / 4 + 2 * h + 1];
+                    const float4 ra = S.rowf[f.ord & (kItems - 1)][r0 / 4 + 2 * h], rb = S.rowf[f.ord & (kItems - 1)][r0 / 4 + 2 * h + 1];
                     const float2 rf[4] = {make_float2(ra.x, ra.y), make_float2(ra.z, ra.w), make_float2(rb.x, rb.y),
                                           make_float2(rb.z, rb.w)};
 #pragma unroll
@@ -769,9 +805,9 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                         unseen &= x[r] == -INFINITY;
                         hidden |= x[r] == -INFINITY;
                     }
-                    if (hidden) {
-                        const int vs = i % Sh::kVStages;
-                        wait(&S.v_full[vs], (i / Sh::kVStages) & 1, ok);
+                    const int vs = i % Sh::kVStages;
+                    if (hidden) wait(&S.v_full[vs], (i / Sh::kVStages) & 1, ok);
+                    if (hidden && ok) {
                         uint4 *vrow = reinterpret_cast<uint4 *>(vring + vs * kTileBytes + me * kPD);
                         uint32_t nan = 0;
 #pragma unroll
@@ -793,7 +829,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                 }
             }
             const float vmax = f.vmax;
-            bool flush = (flags & kGroupFirst) || chain >= (kInt ? kChainInt8 : kChainE4m3) || vmax > vref || (vmax > 0.0f && vmax < vref * kVRange);
+            bool flush = !ok || (flags & kGroupFirst) || chain >= (kInt ? kChainInt8 : kChainE4m3) || vmax > vref || (vmax > 0.0f && vmax < vref * kVRange);
 #pragma unroll
             for (int h = 0; h < kRW / 4; ++h) {
                 const float4 m = S.m[g][r0 / 4 + h];
@@ -806,13 +842,14 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     const float y = redux_max(x[r]);
                     if (lane == 0) S.wmax[g][w4][r0 + r] = y;
                 }
+                // the maxima of all warps are there; the group ends together when a wait of one of its threads has run out
+                if (any_of<kGroup>(!ok, g)) break;
                 if (chain > 0) {
                     wait(&S.p_empty[g], ((i - 2) >> 1) & 1, ok);  // PV of this group's last tile
                     tc_fence_after_sync();
                     add_sums<R, KIND>(to, vref, o);
                     tc_fence_before_sync();
                 }
-                any_of<kGroup>(false, g);  // the maxima of all warps are there
                 // each row's new reference, and what it makes of the sums so far
                 if (gt < R) {
                     const float m = reinterpret_cast<const float *>(S.m[g])[gt];
@@ -996,6 +1033,10 @@ cudaError_t launch_rows(const AttnParams &p, const CacheMaps &maps, int ctas, cu
 }
 
 }  // namespace
+
+cudaError_t set_paged_wait_budget(long long cycles) {
+    return cudaMemcpyToSymbol(g_wait_budget, &cycles, sizeof(cycles));
+}
 
 void paged_copies(const int32_t *at, int32_t *size) {
     unsigned follows = 0;

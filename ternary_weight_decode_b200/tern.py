@@ -164,6 +164,7 @@ def lib() -> ctypes.CDLL:
                 "tern_attention_paged": (ctypes.c_int, [p, i32, i32, p, p, i32, i32, ctypes.c_float, p, i32, p,
                                                         sz, p]),
                 "tern_debug_paged_copies": (ctypes.c_int, [p, p]),
+                "tern_debug_paged_wait_budget": (ctypes.c_int, [i64]),
                 "tern_gemv_fused": (ctypes.c_int, [pm, p, i32, p, i32, i32, i32, p, p, i32, p, i32, p]),
                 "tern_gateup_swiglu_fused": (ctypes.c_int, [pm, pm, p, i32, p, i32, i32, i32, p, i32,
                                                             p, i32, p]),
@@ -830,6 +831,11 @@ def tern_debug_paged_copies(at) -> list[int]:
     size = (ctypes.c_int32 * 8)()
     _check(lib().tern_debug_paged_copies((ctypes.c_int32 * 8)(*at), size), "tern_debug_paged_copies")
     return list(size)
+
+
+def tern_debug_paged_wait_budget(cycles: int):
+    """SM cycles after which a wait of the paged attention gives up; 0: the usual budget."""
+    _check(lib().tern_debug_paged_wait_budget(cycles), "tern_debug_paged_wait_budget")
 
 
 ENGINE_TENSOR_CORES, ENGINE_CUDA_CORES = 0, 1

@@ -55,3 +55,8 @@ def test_runs_are_copied_together():
 @pytest.mark.parametrize("at,size", [(None, 4096), (4096, None)])
 def test_null_pointers_are_refused(at, size):
     assert _lib().tern_debug_paged_copies(at, size) == 1
+
+
+@pytest.mark.parametrize("cycles", [-1, 10 ** 9 + 1])
+def test_wait_budgets_out_of_range_are_refused(cycles):
+    assert _lib().tern_debug_paged_wait_budget(cycles) == 1
