@@ -204,10 +204,8 @@ __device__ __forceinline__ uint32_t e4m3_digit(float2 &x) {
 // the copies or products that it has in flight.  Those that wait for it run out
 // in turn, so the CTA ends, its tensor memory is given back, and its rows may
 // hold anything.
-__device__ long long g_wait_budget = kWaitBudgetCycles;  // (a test shortens it)
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity) {
-    return mbar_wait_bounded(bar, parity, *const_cast<volatile long long *>(&g_wait_budget));
-}
+__constant__ long long c_wait_budget = kWaitBudgetCycles;  // (a test shortens it)
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, c_wait_budget); }
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
     if (ok && !mbar_try_wait(bar, parity)) ok = wait_slow(bar, parity);
 }
@@ -1035,7 +1033,7 @@ cudaError_t launch_rows(const AttnParams &p, const CacheMaps &maps, int ctas, cu
 }  // namespace
 
 cudaError_t set_paged_wait_budget(long long cycles) {
-    return cudaMemcpyToSymbol(g_wait_budget, &cycles, sizeof(cycles));
+    return cudaMemcpyToSymbol(c_wait_budget, &cycles, sizeof(cycles));
 }
 
 void paged_copies(const int32_t *at, int32_t *size) {
