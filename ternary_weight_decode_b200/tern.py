@@ -580,7 +580,8 @@ class _Described:
         self.__dict__.pop("_kept", None)
 
     def described(self):
-        """(address of the struct, device index, the struct)"""
+        """(address of the struct, device index, the struct).  Whoever passes the address on holds the
+        tuple until the call has returned: another thread may meanwhile have a new struct made."""
         kept = self.__dict__.get("_kept")
         if kept is None or [f() for f in kept[1]] != kept[2]:
             s, probes = self.struct(), self.probes()
@@ -680,8 +681,8 @@ def tern_rope_table(theta: float, scale: float, table: torch.Tensor, stream=None
 def tern_rope(rope: RopePlan, pos: torch.Tensor, x: torch.Tensor, y: torch.Tensor, d_invalid=None, stream=None):
     """y [T, H, D] = x rotated by pos int32 [axes, T]; y may be x."""
     T, H, D = x.shape
-    plan, dev, _ = rope.described()
-    st = (_lib or lib()).tern_rope(plan, _positions(pos, dev, rope.axes, T), T, H, D, x.data_ptr(),
+    plan, dev, r = rope.described()
+    st = (_lib or lib()).tern_rope(plan, _positions(pos, dev, r.axes, T), T, H, D, x.data_ptr(),
                                    _heads(x, dev, T, H, D), y.data_ptr(), _heads(y, dev, T, H, D),
                                    _counter(d_invalid, dev), _call_stream(dev, stream))
     if st:
@@ -754,25 +755,25 @@ class PagedBatch(_Described):
 
 
 def _batch_and_cache(batch: PagedBatch, cache: PagedCache):
-    b, dev, _ = batch.described()
-    c, dev_c, _ = cache.described()
-    if dev != dev_c:
-        raise ValueError(f"the batch is on cuda:{dev}, the cache on cuda:{dev_c}")
-    return b, c, dev
+    """What ``described`` gives of both (the caller holds them until its call has returned)."""
+    b, c = batch.described(), cache.described()
+    if b[1] != c[1]:
+        raise ValueError(f"the batch is on cuda:{b[1]}, the cache on cuda:{c[1]}")
+    return b, c
 
 
 def tern_kv_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor, rope: RopePlan,
                          batch: PagedBatch, cache: PagedCache, q_out: torch.Tensor, d_invalid=None, stream=None):
     """q_out [T, Hq, D] = q rotated; k (rotated) and v [T, Hkv, D] quantised into the cache.
     pos int32 [axes, T]; q_out may be q."""
-    T, Hq, Hkv, D = batch.T, q.shape[1], cache.Hkv, cache.D
-    b, c, dev = _batch_and_cache(batch, cache)
-    plan, dev_r, _ = rope.described()
+    (b, dev, bs), (c, _, cs) = _batch_and_cache(batch, cache)
+    plan, dev_r, r = rope.described()
+    T, Hq, Hkv, D = bs.T, q.shape[1], cs.Hkv, cs.D
     if dev_r != dev:
         raise ValueError(f"the rotary table is on cuda:{dev_r}, the batch on cuda:{dev}")
     st = (_lib or lib()).tern_kv_append_paged(
         q.data_ptr(), _heads(q, dev, T, Hq, D), Hq, k.data_ptr(), _heads(k, dev, T, Hkv, D), v.data_ptr(),
-        _heads(v, dev, T, Hkv, D), _positions(pos, dev, rope.axes, T), plan, b, c, q_out.data_ptr(),
+        _heads(v, dev, T, Hkv, D), _positions(pos, dev, r.axes, T), plan, b, c, q_out.data_ptr(),
         _heads(q_out, dev, T, Hq, D), _counter(d_invalid, dev), _call_stream(dev, stream))
     if st:
         _check(st, "tern_kv_append_paged")
@@ -781,8 +782,8 @@ def tern_kv_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos:
 def tern_kv_read_paged(batch: PagedBatch, cache: PagedCache, k_out: torch.Tensor, v_out: torch.Tensor,
                        d_invalid=None, stream=None):
     """k_out, v_out [T, Hkv, D] = the cache's values of the batch's rows."""
-    b, c, dev = _batch_and_cache(batch, cache)
-    T, H, D = batch.T, cache.Hkv, cache.D
+    (b, dev, bs), (c, _, cs) = _batch_and_cache(batch, cache)
+    T, H, D = bs.T, cs.Hkv, cs.D
     st = (_lib or lib()).tern_kv_read_paged(b, c, k_out.data_ptr(), _heads(k_out, dev, T, H, D), v_out.data_ptr(),
                                             _heads(v_out, dev, T, H, D), _counter(d_invalid, dev),
                                             _call_stream(dev, stream))
@@ -792,7 +793,7 @@ def tern_kv_read_paged(batch: PagedBatch, cache: PagedCache, k_out: torch.Tensor
 
 def tern_attention_paged_workspace_bytes(Hq: int, cache: PagedCache) -> int:
     n = ctypes.c_size_t()
-    c, dev, _ = cache.described()
+    c, dev, _struct = cache.described()
     _call_stream(dev, None)  # (the answer is the current device's)
     _check(lib().tern_attention_paged_workspace_bytes(Hq, c, ctypes.byref(n)),
            "tern_attention_paged_workspace_bytes")
@@ -811,8 +812,8 @@ def tern_attention_paged(q: torch.Tensor, batch: PagedBatch, cache: PagedCache, 
                          stream=None):
     """out [T, Hq, D] = causal attention of the batch's rows q over the cache;
     window tokens (0: all) and the first `sinks` are visible; scale 1/sqrt(D) by default."""
-    T, Hq, D = batch.T, q.shape[1], cache.D
-    b, c, dev = _batch_and_cache(batch, cache)
+    (b, dev, bs), (c, _, cs) = _batch_and_cache(batch, cache)
+    T, Hq, D = bs.T, q.shape[1], cs.D
     if workspace.get_device() != dev:
         raise ValueError(f"the workspace is on {workspace.device}, the batch on cuda:{dev}")
     assert workspace.is_contiguous()
