@@ -565,8 +565,8 @@ def tern_attention_decode_q4_0(q: torch.Tensor, cache: KVCache, L: int, out: tor
 # ------------------------------------------------------------------ rotary embedding, paged KV cache
 # The calls below run once per layer and token, so they cost the host little:
 # the descriptors' structs are made and checked once (again when a field is
-# replaced, or a tensor's memory or size), and each call checks its tensors with
-# a few cheap queries.
+# replaced, or a tensor's address or number of elements changes in place), and
+# each call checks its tensors with a few cheap queries.
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
@@ -657,8 +657,8 @@ class RopePlan(_Described):
 
     def probes(self) -> tuple:
         if self.sections is None:
-            return self.table.data_ptr, self.table.numel
-        return self.table.data_ptr, self.table.numel, lambda: tuple(self.sections)
+            return self.table.data_ptr, self.table.size
+        return self.table.data_ptr, self.table.size, lambda: tuple(self.sections)
 
     def struct(self) -> tern_rope_plan:
         t = self.table
@@ -715,8 +715,9 @@ class PagedCache(_Described):
         return _one_device(self.k_codes, self.k_scales, self.v_codes, self.v_scales)
 
     def probes(self) -> tuple:
-        return (self.k_codes.data_ptr, self.k_scales.data_ptr, self.v_codes.data_ptr, self.v_scales.data_ptr,
-                self.k_codes.numel)
+        # (with the heads, page size and D, which are fields, the numbers of elements give the shapes)
+        tensors = self.k_codes, self.k_scales, self.v_codes, self.v_scales
+        return *(t.data_ptr for t in tensors), *(t.numel for t in tensors)
 
     def struct(self) -> tern_paged_cache:
         n = self.k_codes.shape[0]
@@ -744,7 +745,8 @@ class PagedBatch(_Described):
         return _one_device(self.row_start, self.ctx, self.pages)
 
     def probes(self) -> tuple:
-        return (self.row_start.data_ptr, self.ctx.data_ptr, self.pages.data_ptr, self.ctx.numel, self.pages.numel)
+        tensors = self.row_start, self.ctx, self.pages  # (ctx and pages have a row per sequence: their numbers give ld)
+        return *(t.data_ptr for t in tensors), *(t.numel for t in tensors)
 
     def struct(self) -> tern_paged_batch:
         B = self.ctx.shape[0]

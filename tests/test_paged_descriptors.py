@@ -97,3 +97,43 @@ def test_a_call_takes_its_sizes_from_the_struct_it_passes(tern, monkeypatch):
     q = torch.zeros(3, 4, 128)
     tern.tern_attention_paged(q, batch, cache, torch.zeros_like(q), torch.zeros(4096))
     assert seen == [(3, 2)]
+
+
+@pytest.mark.parametrize("name", ["k_codes", "k_scales", "v_codes", "v_scales"])
+def test_a_cache_tensor_resized_in_place_is_refused(tern, name):
+    _, cache, _ = descriptors(tern)
+    cache.described()
+    t = getattr(cache, name)
+    at = t.data_ptr()
+    t.resize_(2, *t.shape[1:])
+    assert t.data_ptr() == at
+    with pytest.raises(AssertionError):
+        cache.described()
+
+
+@pytest.mark.parametrize("name", ["row_start", "ctx", "pages"])
+def test_a_batch_tensor_resized_in_place_is_refused(tern, name):
+    _, _, batch = descriptors(tern)
+    batch.described()
+    t = getattr(batch, name)
+    at = t.data_ptr()
+    t.resize_(1, *t.shape[1:])
+    assert t.data_ptr() == at
+    with pytest.raises(AssertionError):
+        batch.described()
+
+
+def test_tensors_resized_together_are_followed(tern):
+    plan, cache, batch = descriptors(tern)
+    for d in (plan, cache, batch):
+        d.described()
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        t.resize_(2, *t.shape[1:])
+    batch.row_start.resize_(2), batch.ctx.resize_(1), batch.pages.resize_(1, 2)
+    plan.table.resize_(8, 32, 2)
+    plan.sections[:] = [20, 12]
+    assert cache.described()[2].n_pages == 2
+    assert (batch.described()[2].B, batch.described()[2].pages_ld) == (1, 2)
+    assert plan.described()[2].rot_dim == 64
+    plan.table.resize_(4, 64, 2)   # the same number of elements
+    assert (plan.described()[2].n_pos, plan.described()[2].rot_dim) == (4, 128)
