@@ -579,6 +579,9 @@ class _Described:
         object.__setattr__(self, name, value)
         self.__dict__.pop("_kept", None)
 
+    def __getstate__(self):  # copies and pickles make a struct of their own
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}
+
     def described(self):
         """(address of the struct, device index, the struct).  Whoever passes the address on holds the
         tuple until the call has returned: another thread may meanwhile have a new struct made."""

@@ -2,8 +2,10 @@
 a call passes on stay alive until it returns, whatever other threads do to the
 descriptors meanwhile.  A stand-in takes the library's place; tensors are the
 CPU's."""
+import copy
 import ctypes
 import gc
+import pickle
 import weakref
 
 import pytest
@@ -137,3 +139,15 @@ def test_tensors_resized_together_are_followed(tern):
     assert plan.described()[2].rot_dim == 64
     plan.table.resize_(4, 64, 2)   # the same number of elements
     assert (plan.described()[2].n_pos, plan.described()[2].rot_dim) == (4, 128)
+
+
+@pytest.mark.parametrize("copied", [copy.copy, copy.deepcopy, lambda d: pickle.loads(pickle.dumps(d))])
+def test_descriptors_that_were_used_are_copied(tern, copied):
+    for d in descriptors(tern):
+        address, _, kept = d.described()
+        other = copied(d)
+        assert type(other) is type(d) and "_kept" not in other.__dict__
+        assert other.described()[0] != address and d.described()[2] is kept
+        for name, t in other.__dict__.items():
+            if isinstance(t, torch.Tensor):
+                assert torch.equal(t, getattr(d, name))
