@@ -351,6 +351,15 @@ __device__ __forceinline__ void append_block(const AppendParams &p, int b, int b
     const float top = fmaxf(fmaxf(shared_max[0], shared_max[1]), fmaxf(shared_max[2], shared_max[3]));
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(is_k ? 1 : 2) : "memory");  // the words are free for the next block
     if (bi0 < 0) return;
+    if (KIND == TERN_KV_INT8 && top > 0x1.FCp126f) {  // past 127 of the largest scale the code is 127 or -127, not -128
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[i][e] = fmaxf(a[i][e], -0x1.FCp126f);
+                c8[i][e] = fmaxf(c8[i][e], -0x1.FCp126f);
+            }
+    }
     uint8_t *cp = (is_k ? v.kc : v.vc) + bi * (kPB * kPD);
     float scale = pow2_scale<KIND>(top);
     if (slot0 > 0) {  // earlier tokens: keep their scale, or rescale their codes
