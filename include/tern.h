@@ -635,10 +635,14 @@ tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_ca
  * Sums and softmax statistics are held in fp32 (products and partial sums of
  * int8 codes exactly in int32), and the order of every sum is fixed by the
  * lengths: the same inputs give the same bits.  A query is held to 2^-24 of its
- * row's largest element (int8) or 2^-20 of each element (e4m3); a softmax
- * weight times its block's value scale to 2^-27 of the largest weight times the
- * largest value scale around it (int8; scales 256 times smaller or more begin
- * anew) or 2^-20 of itself (e4m3).  A query row with a NaN or
+ * row's largest element (int8) or 2^-20 of each element (e4m3).  A softmax
+ * weight times its block's value scale is held to 2^-27 of a reference (int8),
+ * or to 2^-20 of itself and 2^-28 of the reference (e4m3).  The reference is
+ * the row's largest such product so far; it falls to that of the present 128
+ * tokens where theirs lies more than 2^12 below, in the tokens behind one that
+ * stands out by 2^12 and else after 4096 to 8192 tokens (at most 2^48 in all):
+ * a first token of a large weight and a small value costs the others nothing.
+ * A query row with a NaN or
  * an infinity gives NaN, as does a NaN code (e4m3) for the rows that see its
  * token; scales of visible blocks must be positive and finite, as the append
  * writes them, and what lies behind a sequence's last token may hold anything.

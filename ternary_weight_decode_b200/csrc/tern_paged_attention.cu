@@ -15,8 +15,8 @@
 //    signed 8-bit digits, q = d2 2^16 + d1 2^8 + d0 (error at most 2^-24 of the
 //    row's largest element): three columns of the B operand per row.  A digit's
 //    product is an exact int32 below 2^21.
-//  * A softmax weight times its block's value scale, relative to a reference of
-//    each, is an unsigned 32-bit fixed-point number, and its four bytes are
+//  * A softmax weight times its block's value scale, relative to the row's
+//    reference, is an unsigned 32-bit fixed-point number, and its four bytes are
 //    four unsigned digits: the word is stored as it is, four columns per row.
 //    The sums over tokens are exact int32, so they stay in tensor memory from
 //    tile to tile.
@@ -24,18 +24,28 @@
 //  * A query row is scaled below 2^8 and each element written as five e4m3
 //    digits, x = d0 + (d1 + (d2 + ...) / 16) / 16, each the nearest to what is
 //    left: a digit is off by 2^-4 of it, so the five by 2^-20 of the element.
-//  * A softmax weight times its block's value scale, below 2^8 (2^2 for a new
-//    reference's largest score), likewise: off by 2^-20 of itself or, where the
-//    digits' subnormals begin, 2^-26.
+//  * A softmax weight times its block's value scale, relative to the row's
+//    reference below 2^8 (2^2 for a new reference's largest), likewise: off by
+//    2^-20 of itself or, where the digits' subnormals begin, 2^-26.
 //    The fp32 sums stay in tensor memory for at most 16 tiles.
 //  A weight of 0 does not undo a NaN code: value rows that some query row does
 //  not see (the rest of a block may hold anything) lose theirs in shared memory.
-// References: row r's weights are 2^(score - m_r) with m_r at least the largest
-// score so far; when a tile has a larger one (or block scales leave the
-// reference's range, or a chain of sums ends), the sums are read, added to fp32
-// registers and begun again.  m_r is set six above the largest score, so that
-// happens a few times per item (26 of int8's 32 bits remain; block scales may
-// cost 8 more).
+// References: the digits hold the product 2^y of a row's weight and the token's
+// value scale, y = score + log2(scale) (its exponent, relative to that of the
+// item; the mantissa is multiplied on), as 2^(y - m_r) with m_r at least the
+// largest y so far, and z sums 2^(y - m_r) / scale.  When a tile has a larger y,
+// or a chain of sums ends, the sums are read, added to fp32 registers and begun
+// again.  m_r is set six above the largest y, so that happens a few times per
+// item (26 of int8's 32 bits remain).
+// With weights and scales held by references of their own, a first token of a
+// large weight and a small value (what sinks are kept for) set both against
+// itself: at 65536 tokens, a score 2^27.5 above the rest and a value scale of
+// 1/64, what the others' weights lost was 6.6e-3 of the output.  So a reference
+// may fall as well: new references are taken from the present tile, wherever
+// that one's largest y lies 12 or more below the one that set m_r; and they are
+// taken behind a y that stands 12 above what came before it or above another 32
+// tokens of its tile, and when a chain ends.  (A test of every eighth tile cost
+// prompts 12 %.)  The error is then below that of plain fp32 on such inputs too.
 //
 // One CTA per SM.  Warps of their own look the tiles up, copy K, copy V, issue
 // QK, issue PV and make the query digits: a thread takes some 450 cycles to
@@ -63,6 +73,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <float.h>
+
 #include <algorithm>
 
 #include "tern_paged_attention.cuh"
@@ -79,9 +91,12 @@ constexpr int kItems = 16;                // items kept for the query warp, and 
                                           // may be item t, is noted before the scales of t - 11 are: at least 10, or the
                                           // look-up waits for digits that wait for it)
 constexpr float kHeadroom = 6.0f;         // a new reference lies this far (log2) above the largest score
-constexpr int kChainInt8 = 256;           // tiles summed in int32: 256 * 128 * 255 * 127 < 2^31
+constexpr int kChainInt8 = 32;            // tiles summed in int32, at most 256: 256 * 128 * 255 * 127 < 2^31
 constexpr int kChainE4m3 = 16;            // tiles summed in fp32 inside the tensor cores (16 or 64: the same time)
-constexpr float kVRange = 1.0f / 256.0f;  // largest block scale of a tile, relative to the reference
+constexpr float kFallBelow = 18.0f;       // a reference this far above a tile's largest product falls (12 below what set it)
+constexpr float kLowest = 48.0f;          // how far references may fall below the highest
+constexpr int kScaleRange = 24;           // largest block scale of a tile (log2), relative to the item's
+constexpr int kScaleLowest = -30;         // least block scale that a reference is told apart by
 
 template <int R, int KIND>
 struct Shape {
@@ -95,6 +110,7 @@ struct Shape {
     static constexpr bool kCopyWarps = kHelpers == 8;
     static constexpr int kWarpLook = 0, kWarpK = kCopyWarps ? 1 : -1, kWarpV = kCopyWarps ? 2 : -1,
                          kWarpQK = kCopyWarps ? 3 : 1, kWarpPV = kCopyWarps ? 4 : 2, kWarpQ = kCopyWarps ? 5 : 3;
+    static constexpr int kQWarps = kCopyWarps ? 3 : 1;  // from kWarpQ on
     static constexpr int kSBufs = R == 32 ? 2 : 4;    // S accumulators
     static constexpr int kQD = kInt ? 3 : 5;          // digits of a query, columns of S per row
     static constexpr int kVD = kInt ? 4 : 5;         // digits of a weight, columns of O per row
@@ -114,13 +130,14 @@ struct Shape {
 
 // One tile, as the softmax and MMA warps see it.
 struct TileInfo {
-    float ks[kTB], vs[kTB];
+    float ks[kTB], vm[kTB];
+    int ve[kTB];      // value scales: 2^ve times vm, which is in (1/2, 1] (0: no scale) times what a weight of 1 is held as
     int j0[kTB];      // first token of each block
     int row[kTB];     // its first code row, for the block that begins a copy
     int size[kTB];    // log2 of the blocks that this copy takes, -1: none begins here
     int valid;        // bit j: block j is there
     int flags;
-    float vmax;       // largest value scale
+    int vtop;         // largest ve
     int head, rt, k, units, ord;
     Seq s;
 };
@@ -146,7 +163,7 @@ struct AttnShared {
     TileInfo info[kInfo];
     ItemInfo item[kItems], first_item;
     float4 rowf[kItems][R / 4];        // score scale of each row's digits
-    float4 m[2][R / 4], mref[2][R / 4];  // each group's references; mref: 0 for a row that has seen nothing
+    float4 m[2][R / 4], top[2][R / 4];  // each group's references, and the highest they have been
     float4 back[2][R / 4];            // what new references make of the sums before
     float wmax[2][4][R];
     float zsum[2][4][R];
@@ -219,6 +236,9 @@ __device__ __forceinline__ float small_int(uint32_t c) {
     return __uint_as_float(c + 0x4B400000u) - 12582912.0f;
 }
 
+// 2^e, -127 < e < 128; 0 below.
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(max(127 + e, 0)) << 23); }
+
 __device__ __forceinline__ uint32_t to_u32_sat(float x) {
     uint32_t u;
     asm("cvt.rni.u32.f32 %0, %1;" : "=r"(u) : "f"(x));
@@ -229,6 +249,12 @@ __device__ __forceinline__ float redux_max(float x) {
     float y;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Whether a tile whose largest value scale is 2^vtop needs another value
+// reference than 2^lref.
+__device__ __forceinline__ bool other_scale(int vtop, int lref) {
+    return vtop > -127 && static_cast<unsigned>(vtop - lref + kScaleRange) > 2 * kScaleRange;
 }
 
 // Barrier over the N threads of softmax group g, with the "or" of x.
@@ -346,6 +372,9 @@ __device__ __forceinline__ void copy_codes(const CacheMaps &maps, AttnShared<R, 
     copies_land<R, KIND, K>(S, n);
 }
 
+// (Out of line: with at most kLineThreads sequences they are in shared memory.)
+__device__ __noinline__ Seq far_sequence(const AttnParams &p, int b) { return sequence(p, b); }
+
 // Look-up of a range's tiles: writes the infos of the items and tiles.  Four
 // tiles at a time (lane = 8 * tile + block), in three steps that overlap, so
 // that no load is waited for while another could be on its way: page numbers;
@@ -443,14 +472,17 @@ __device__ __forceinline__ void look_up(const AttnParams &p, const CacheMaps &ma
         // ---- tiles i0 - 8 ..: scales
         if (i0 >= 8) {
             const int i = i0 - 8 + sub;
-            float vmax = vs_now;
+            // the exponent rounded up; of no scale (0), and of subnormal ones, -127
+            const int ve = min(127, static_cast<int>((__float_as_uint(vs_now) + 0x7FFFFFu) >> 23) - 127);
+            int vtop = ve;
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+            for (int o = 1; o < 8; o <<= 1) vtop = max(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
             if (i < count) {
                 TileInfo &f = S.info[i % kInfo];
                 f.ks[j] = ks_now;
-                f.vs[j] = vs_now;
-                if (j == 0) f.vmax = vmax;
+                f.vm[j] = vs_now * exp2i(-ve) * (Shape<R, KIND>::kInt ? 0x1p32f : 0x1p8f);
+                f.ve[j] = ve;
+                if (j == 0) f.vtop = vtop;
             }
             __syncwarp();
             if (j == 0 && i < count) mbar_arrive(&S.scales_full[i % kInfo]);
@@ -521,7 +553,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.p_full[i], 4 * Sh::kHalves);
             mbar_init(&S.p_empty[i], 1);
-            mbar_init(&S.q_full[i], 1);
+            mbar_init(&S.q_full[i], Sh::kQWarps);
             mbar_init(&S.q_empty[i], 1);
             S.cut[i].valid = 0;
         }
@@ -534,7 +566,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&S.item_full[i], 1);
-            mbar_init(&S.item_empty[i], 1);
+            mbar_init(&S.item_empty[i], Sh::kQWarps);
         }
         for (int i = 0; i < Sh::kSBufs; ++i) {
             mbar_init(&S.s_full[i], 2);
@@ -563,7 +595,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
     if (count == 0) {
     } else if (warp == Sh::kWarpLook) {
         look_up<R, KIND>(p, maps, S, kring, vring, L, ranges, u0, count,
-                         [&](int b) { return L.per == 1 ? S.line.seq[b] : sequence(p, b); });
+                         [&](int b) { return L.per == 1 ? S.line.seq[b] : far_sequence(p, b); });
     } else if (warp == Sh::kWarpK) {
         copy_codes<R, KIND, true>(maps, S, kring, count);
     } else if (warp == Sh::kWarpV) {
@@ -634,7 +666,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == Sh::kWarpQ) {
+    } else if (warp >= Sh::kWarpQ && warp < Sh::kWarpQ + Sh::kQWarps) {
         // ---- query digits of each item, ahead of its tiles
 #pragma unroll 1
         for (int done = 0, item = 0; done < count; ++item) {
@@ -644,22 +676,33 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
             if (!all_ok(ok)) break;
             const ItemInfo it = S.item[slot];
             uint8_t *qb = qbuf + (item & 1) * Sh::kQBytes;
+            // one or two rows at a time, the next ones on their way (a loop of four rows written out crowds the
+            // instruction cache)
+            constexpr int kAt = Sh::kQWarps == 1 ? 2 : 1, kStep = kAt * Sh::kQWarps;
+            auto load_row = [&](int rr) {
+                const int row = R * it.rt + rr, ri = p.by_gq.quot(row);
+                if (rr >= R || row >= it.s.rows) return make_float4(0, 0, 0, 0);
+                return *reinterpret_cast<const float4 *>(p.q + static_cast<int64_t>(it.s.start + ri) * p.ldq +
+                                                         (it.head * p.GQ + row - ri * p.GQ) * kPD + 4 * lane);
+            };
+            float4 x[kAt], next[2][kAt];
+            const int first = kAt * (warp - Sh::kWarpQ);
+#pragma unroll
+            for (int h = 0; h < kAt; ++h) {
+                next[0][h] = load_row(first + h);
+                next[1][h] = load_row(first + kStep + h);
+            }
 #pragma unroll 1
-            for (int rr0 = 0; rr0 < R; rr0 += 4) {
-                float4 x[4];
-                float up[4], down[4];
+            for (int rr0 = first; rr0 < R; rr0 += kStep) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int row = R * it.rt + rr0 + h;
-                    x[h] = make_float4(0, 0, 0, 0);
-                    if (row < it.s.rows) {
-                        const int ri = p.by_gq.quot(row);
-                        x[h] = *reinterpret_cast<const float4 *>(p.q + static_cast<int64_t>(it.s.start + ri) * p.ldq +
-                                                                 (it.head * p.GQ + row - ri * p.GQ) * kPD + 4 * lane);
-                    }
+                for (int h = 0; h < kAt; ++h) {
+                    x[h] = next[0][h];
+                    next[0][h] = next[1][h];
+                    next[1][h] = load_row(rr0 + 2 * kStep + h);
                 }
+                float up[kAt];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < kAt; ++h) {
                     // (the largest bits: those of a NaN or an infinity lie above all others)
                     const uint32_t amax = __reduce_max_sync(
                         0xffffffffu, max(max(__float_as_uint(fabsf(x[h].x)), __float_as_uint(fabsf(x[h].y))),
@@ -668,14 +711,16 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     // [2^7, 2^8), below the largest e4m3 value
                     const int e = max(-120, min(120, (kInt ? 148 : 134) - static_cast<int>(amax >> 23)));
                     up[h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                    down[h] = R * it.rt + rr0 + h < it.s.rows
-                                  ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
-                                  : 0.0f;
-                    if (amax >= 0x7F800000u) down[h] = NAN;  // no digits hold such a row: all its scores are NaN
+                    if (lane == 0) {
+                        float down = R * it.rt + rr0 + h < it.s.rows
+                                         ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                                         : 0.0f;
+                        if (amax >= 0x7F800000u) down = NAN;  // no digits hold such a row: all its scores are NaN
+                        reinterpret_cast<float *>(S.rowf[slot])[rr0 + h] = down;
+                    }
                 }
-                if (lane == 0) S.rowf[slot][rr0 / 4] = make_float4(down[0], down[1], down[2], down[3]);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < kAt; ++h) {
                     const int rr = rr0 + h;
                     // digit k of the four dimensions as one word; column of digit k of row rr: 2 kQD (rr / 2) + 2 k + rr % 2,
                     // so that two rows' digits are neighbours
@@ -701,8 +746,8 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     }
 #pragma unroll
                     for (int k = 0; k < Sh::kQD; ++k)
-                        *reinterpret_cast<uint32_t *>(
-                            qb + sw128_offset(2 * Sh::kQD * (rr >> 1) + 2 * k + (rr & 1), 4 * lane)) = w[k];
+                        *reinterpret_cast<uint32_t *>(qb + sw128_offset(2 * Sh::kQD * (rr >> 1) + 2 * k + (rr & 1), 4 * lane)) =
+                            w[k];
                 }
             }
             fence_proxy_async_smem();
@@ -723,7 +768,8 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
         uint8_t *my_p = pbuf + g * Sh::kPBytes;
         float2 z[kRW / 2];
         float o[kRW];
-        float vref = 1.0f, inv_vref = 1.0f;
+        int lref = 0;   // value reference (log2)
+        bool again = false;  // the next tile takes new references, in case they fall
         int chain = 0, k_first = 0;
         int handovers = 0;  // items of which both groups had parts
 #pragma unroll 1
@@ -739,17 +785,15 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                 for (int r = 0; r < kRW; ++r) o[r] = 0.0f;
 #pragma unroll
                 for (int r = 0; r < kRW / 2; ++r) z[r] = make_float2(0.0f, 0.0f);
-                if (gt < R) {
-                    reinterpret_cast<float *>(S.m[g])[gt] = -INFINITY;
-                    reinterpret_cast<float *>(S.mref[g])[gt] = 0.0f;
-                }
-                // (no barrier: whatever the others find in m, they take new references below)
+                lref = f.vtop;
+                if (gt < R)  // (no barrier: whatever the others find in m, they take new references below)
+                    reinterpret_cast<float *>(S.m[g])[gt] = reinterpret_cast<float *>(S.top[g])[gt] = -FLT_MAX;
             }
-            // scores of this token, in log2
+            // scores of this token plus its value scale, in log2: the products that the weights' digits hold
             float x[kRW];
             {
-                const float ks = f.ks[me >> 4];
-                const float2 ks2 = make_float2(ks, ks);
+                const float ks = f.ks[me >> 4], lvf = small_int(max(f.ve[me >> 4] - lref, kScaleLowest));
+                const float2 ks2 = make_float2(ks, ks), lv2 = make_float2(lvf, lvf);
 #pragma unroll
                 for (int h = 0; h < kRW / 8; ++h) {
                     uint32_t sv[8 * Sh::kQD];
@@ -775,7 +819,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                             for (int k = 3; k >= 0; --k)
                                 t = __ffma2_rn(t, down, make_float2(__uint_as_float(d[2 * k]), __uint_as_float(d[2 * k + 1])));
                         }
-                        const float2 s2 = __fmul2_rn(t, __fmul2_rn(rf[r], ks2));
+                        const float2 s2 = __ffma2_rn(t, __fmul2_rn(rf[r], ks2), lv2);
                         x[8 * h + 2 * r] = s2.x;
                         x[8 * h + 2 * r + 1] = s2.y;
                     }
@@ -808,7 +852,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     if (hidden && ok) {
                         uint4 *vrow = reinterpret_cast<uint4 *>(vring + vs * kTileBytes + me * kPD);
                         uint32_t nan = 0;
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < kPD / 16; ++k) {
                             uint4 c = vrow[k];
                             uint32_t *w = &c.x;
@@ -826,15 +870,22 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     }
                 }
             }
-            const float vmax = f.vmax;
-            bool flush = !ok || (flags & kGroupFirst) || chain >= (kInt ? kChainInt8 : kChainE4m3) || vmax > vref || (vmax > 0.0f && vmax < vref * kVRange);
+            bool flush = !ok || again || (flags & kGroupFirst) || chain >= (kInt ? kChainInt8 : kChainE4m3) || other_scale(f.vtop, lref);
 #pragma unroll
             for (int h = 0; h < kRW / 4; ++h) {
                 const float4 m = S.m[g][r0 / 4 + h];
                 flush |= x[4 * h] > m.x || x[4 * h + 1] > m.y || x[4 * h + 2] > m.z || x[4 * h + 3] > m.w;
             }
             if (any_of<kGroup>(flush, g)) {
-                // ---- new references: each row's largest score of the tile over all 128 tokens
+                // ---- new references: each row's largest product of the tile over all 128 tokens
+                const int scale_was = lref;
+                if (other_scale(f.vtop, lref)) {  // another value reference from here on
+                    lref = f.vtop;
+                    const int ve = f.ve[me >> 4];
+                    const float by = small_int(max(ve - lref, kScaleLowest) - max(ve - scale_was, kScaleLowest));
+#pragma unroll
+                    for (int r = 0; r < kRW; ++r) x[r] += by;
+                }
 #pragma unroll
                 for (int r = 0; r < kRW; ++r) {
                     const float y = redux_max(x[r]);
@@ -845,22 +896,28 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                 if (chain > 0) {
                     wait(&S.p_empty[g], ((i - 2) >> 1) & 1, ok);  // PV of this group's last tile
                     tc_fence_after_sync();
-                    add_sums<R, KIND>(to, vref, o);
+                    add_sums<R, KIND>(to, exp2i(scale_was), o);
                     tc_fence_before_sync();
                 }
                 // each row's new reference, and what it makes of the sums so far
+                bool far = false;
                 if (gt < R) {
-                    const float m = reinterpret_cast<const float *>(S.m[g])[gt];
-                    const float top = fmaxf(fmaxf(S.wmax[g][0][gt], S.wmax[g][1][gt]),
-                                            fmaxf(S.wmax[g][2][gt], S.wmax[g][3][gt]));
-                    float back = 1.0f;
-                    if (top > m) {
-                        back = ex2(m - (top + kHeadroom));
-                        reinterpret_cast<float *>(S.m[g])[gt] = reinterpret_cast<float *>(S.mref[g])[gt] = top + kHeadroom;
-                    }
-                    reinterpret_cast<float *>(S.back[g])[gt] = back;
+                    float *mp = reinterpret_cast<float *>(S.m[g]) + gt, *hp = reinterpret_cast<float *>(S.top[g]) + gt;
+                    const float w0 = S.wmax[g][0][gt], w1 = S.wmax[g][1][gt], w2 = S.wmax[g][2][gt], w3 = S.wmax[g][3][gt];
+                    const float was = *mp, top = fmaxf(fmaxf(w0, w1), fmaxf(w2, w3));
+                    const float by = static_cast<float>(lref - scale_was), high = *hp - by;
+                    // (o, up to 2^25 value references, is to stay finite when it is raised by the fall)
+                    const float lowest = fminf(fmaxf(70.0f - static_cast<float>(lref), 0.0f), kLowest);
+                    float m = was - by;
+                    // far above what came before it, or what stands beside it
+                    const float low = fminf(fminf(w0, w1), fminf(w2, w3));
+                    far = (top > m + kHeadroom && m > -FLT_MAX) || (low < top - (kFallBelow - kHeadroom) && low > -FLT_MAX);
+                    if (top > m || (top < m - kFallBelow && top > -FLT_MAX)) m = fmaxf(top + kHeadroom, high - lowest);
+                    *mp = m;
+                    *hp = fmaxf(high, m);
+                    reinterpret_cast<float *>(S.back[g])[gt] = ex2(was - m);
                 }
-                any_of<kGroup>(false, g);
+                again = any_of<kGroup>(far, g);
                 if (!(flags & kGroupFirst)) {
 #pragma unroll
                     for (int h = 0; h < kRW / 4; ++h) {
@@ -872,26 +929,25 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                         z[2 * h + 1] = __fmul2_rn(z[2 * h + 1], make_float2(back.z, back.w));
                     }
                 }
-                if (vmax > 0.0f) {
-                    vref = vmax;
-                    inv_vref = recip(vmax);
-                }
                 chain = 0;
             }
             // weights and their digits
-            const float up = f.vs[me >> 4] * inv_vref * (kInt ? 0x1p32f : 0x1p8f);
-            const float2 up2 = make_float2(up, up);
+            const int lv = f.ve[me >> 4] - lref;
+            float up = f.vm[me >> 4];
+            if (lv < kScaleLowest) up *= exp2i(lv - kScaleLowest);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - max(lv, kScaleLowest)) << 23);
+            const float2 up2 = make_float2(up, up), down2 = make_float2(down, down);
             wait(&S.p_empty[g], ((i >> 1) + 1) & 1, ok);  // PV of this group's last tile has read the buffer
             uint8_t *row = my_p + me * Sh::kPRow;
             float2 u[kRW / 2];
 #pragma unroll
             for (int h = 0; h < kRW / 4; ++h) {
-                const float4 m = S.mref[g][r0 / 4 + h];
+                const float4 m = S.m[g][r0 / 4 + h];
                 const float2 x0 = __fadd2_rn(make_float2(x[4 * h], x[4 * h + 1]), make_float2(-m.x, -m.y));
                 const float2 x1 = __fadd2_rn(make_float2(x[4 * h + 2], x[4 * h + 3]), make_float2(-m.z, -m.w));
                 const float2 w0 = make_float2(ex2(x0.x), ex2(x0.y)), w1 = make_float2(ex2(x1.x), ex2(x1.y));
-                z[2 * h] = __fadd2_rn(z[2 * h], w0);
-                z[2 * h + 1] = __fadd2_rn(z[2 * h + 1], w1);
+                z[2 * h] = __ffma2_rn(w0, down2, z[2 * h]);
+                z[2 * h + 1] = __ffma2_rn(w1, down2, z[2 * h + 1]);
                 u[2 * h] = __fmul2_rn(w0, up2);
                 u[2 * h + 1] = __fmul2_rn(w1, up2);
                 if constexpr (kInt)
@@ -936,7 +992,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                 if (lane < kRW) S.zsum[g][w4][r0 + lane] = zw;
                 wait(&S.p_empty[g], (i >> 1) & 1, ok);
                 tc_fence_after_sync();
-                add_sums<R, KIND>(to, vref, o);
+                add_sums<R, KIND>(to, exp2i(lref), o);
                 tc_fence_before_sync();
                 chain = 0;
                 // the sums by dimension: where the weights lay, or, when the other group has the item's last tile, handed
