@@ -634,7 +634,7 @@ tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_ca
  *  may overlap need separate ones.
  * Sums and softmax statistics are held in fp32 (products and partial sums of
  * int8 codes exactly in int32), and the order of every sum is fixed by the
- * lengths: the same inputs give the same bits.  A query is held to 2^-24 of its
+ * lengths: the same inputs give the same bits.  A query is held to 2^-22.9 of its
  * row's largest element (int8) or 2^-20 of each element (e4m3).  A softmax
  * weight times its block's value scale is held to 2^-27 of a reference (int8),
  * or to 2^-20 of itself and 2^-28 of the reference (e4m3).  The reference is

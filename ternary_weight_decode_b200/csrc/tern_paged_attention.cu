@@ -12,9 +12,9 @@
 // 128-byte swizzle), V the same bytes read the other way (M-major).
 // int8 codes (tcgen05.mma kind::i8, exact int32 sums):
 //  * A query row is scaled by a power of two to 23 bits and split into three
-//    signed 8-bit digits, q = d2 2^16 + d1 2^8 + d0 (error at most 2^-24 of the
+//    signed 8-bit digits, q = d2 2^16 + d1 2^8 + d0 (error at most 2^-22.9 of the
 //    row's largest element): three columns of the B operand per row.  A digit's
-//    product is an exact int32 below 2^21.
+//    product is an exact int32 of at most 2^21.
 //  * A softmax weight times its block's value scale, relative to the row's
 //    reference, is an unsigned 32-bit fixed-point number, and its four bytes are
 //    four unsigned digits: the word is stored as it is, four columns per row.
@@ -707,9 +707,10 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     const uint32_t amax = __reduce_max_sync(
                         0xffffffffu, max(max(__float_as_uint(fabsf(x[h].x)), __float_as_uint(fabsf(x[h].y))),
                                          max(__float_as_uint(fabsf(x[h].z)), __float_as_uint(fabsf(x[h].w)))));
-                    // the row times 2^e: its largest value in [2^21, 2^22), so that three signed int8 digits hold it, or in
-                    // [2^7, 2^8), below the largest e4m3 value
-                    const int e = max(-120, min(120, (kInt ? 148 : 134) - static_cast<int>(amax >> 23)));
+                    // the row times 2^e: its largest value in (1.984 * 2^21, 1.984 * 2^22], which three signed int8 digits
+                    // hold (127 * (2^16 + 2^8 + 1) is 1.992 * 2^22), or in [2^7, 2^8), below the largest e4m3 value
+                    const int e = max(-120, min(120, kInt ? 149 - static_cast<int>((amax + 0x1FFFFu) >> 23)
+                                                          : 134 - static_cast<int>(amax >> 23)));
                     up[h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                     if (lane == 0) {
                         float down = R * it.rt + rr0 + h < it.s.rows
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     for (int r = 0; r < 4; ++r) {
                         const uint32_t *d = sv + 2 * Sh::kQD * r;
                         float2 t;
-                        if constexpr (kInt) {  // (d2 2^8 + d1) 2^8 + d0: the first sum is an integer below 2^30, rounded to fp32
+                        if constexpr (kInt) {  // (d2 2^8 + d1) 2^8 + d0: the first sum is an integer of at most 2^29 + 2^21, rounded to fp32
                             t = make_float2(static_cast<float>(static_cast<int>(256 * d[4] + d[2])),
                                             static_cast<float>(static_cast<int>(256 * d[5] + d[3])));
                             t = __ffma2_rn(t, make_float2(256.0f, 256.0f), make_float2(small_int(d[0]), small_int(d[1])));

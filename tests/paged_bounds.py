@@ -106,3 +106,13 @@ def row_by_digits(q, K, V, v_scales, scale, kind, drop_q=0, drop_w=0):
     else:
         u = e4m3_digits(prod * np.exp2(8 - c), 5 - drop_w) / np.exp2(8 - c)
     return (u @ (V / v_scales[:, None])) / w.sum()
+
+
+def border_query(rng):
+    """(q, signs) [D = 128]: a query whose largest element is just 1 and whose others lie half-way between multiples of
+    2^-21; kept to those multiples, all errors would have the signs given, while q . signs is about 0."""
+    m = rng.integers(1 << 17, 1 << 20, 64) * 2
+    m = np.concatenate([m + 1, m])             # odd ones round up, even ones down
+    q = ((2 * m + 1) * 2.0 ** -22).astype(np.float32)
+    q[63], q[127] = 1.0, 1.0 - 2.0 ** -21
+    return q, np.concatenate([np.ones(64), -np.ones(64)])

@@ -9,7 +9,7 @@ import torch
 
 from gpu_util import to_dev
 from oracle import paged
-from paged_bounds import RMS_FACTOR, bound_row, exponent, fp32_row, rms, softmax_row
+from paged_bounds import RMS_FACTOR, border_query, bound_row, exponent, fp32_row, rms, softmax_row
 from test_gpu_paged import D, E4M3, INT8, device_cache, i32, page_table
 from ternary_weight_decode_b200 import tern
 
@@ -163,3 +163,27 @@ def test_a_key_that_outweighs_all_others_gives_its_value(n, ctx, kind):
             # below e^-40 of it each
             assert np.all(np.abs(got[r, h] - v) <= 2.0 ** -20 * np.abs(v) + see * np.exp(-40.0) * np.abs(V[g, :see]).max())
     assert alone >= n * Hq / 2
+
+
+@pytest.mark.parametrize("rows", [1, 9, 40])
+def test_queries_between_the_digits_steps(rows):
+    """int8: a row whose largest element is just a power of two, the others half-way between the steps of 22 bits."""
+    rng = np.random.default_rng(rows)
+    q, signs = zip(*(border_query(rng) for _ in range(rows)))
+    q = np.stack(q)[:, None]
+    code = (100 * signs[0]).astype(np.int8)
+    codes = np.zeros((1, 1, 48, D), np.int8)
+    codes[0, 0, 0], codes[0, 0, 1:16] = code, -code
+    ref = dict(k_codes=codes.view(np.uint8).copy(), k_scales=np.ones((1, 1, 3), np.float32), v_scales=np.ones((1, 1, 3), np.float32))
+    codes[0, 0, 0], codes[0, 0, 1:16] = 100, -100
+    ref["v_codes"] = codes.view(np.uint8)
+    ctx = 2 + rows - 1   # row 0 sees two tokens, the others more of the second kind
+    if rows > 1:
+        ref["k_codes"][0, 0, 2:], ref["v_codes"][0, 0, 2:] = ref["k_codes"][0, 0, 1], ref["v_codes"][0, 0, 1]
+    pages = np.array([[0]], np.int32)
+    got = run(q, np.array([0, rows]), [ctx], pages, device_cache(ref, INT8), INT8)
+    K, V, s = (x[0] for x in sequence(ref, pages, 0, ctx, 48, INT8))
+    for r in range(rows):
+        see = 2 + r
+        tol = bound_row(q[r, 0], K[:see], V[:see], s[:see], SCALE, INT8)
+        assert np.all(np.abs(got[r, 0] - softmax_row(q[r, 0], K[:see], V[:see], SCALE)[2]) <= tol)

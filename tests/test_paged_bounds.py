@@ -3,7 +3,8 @@ its arithmetic: the whole of it keeps them, with a digit less it does not."""
 import numpy as np
 import pytest
 
-from paged_bounds import E4M3, INT8, RMS_FACTOR, bound_row, fp32_row, query_digits, rms, row_by_digits, softmax_row
+from paged_bounds import (E4M3, INT8, RMS_FACTOR, border_query, bound_row, fp32_row, query_digits, rms, row_by_digits,
+                          softmax_row)
 from oracle import paged
 
 D = 128
@@ -59,3 +60,16 @@ def test_query_digits():
         assert np.abs(query_digits(q, INT8) - q).max() <= 2.0 ** -22.9 * np.abs(q).max()
         e = np.abs(query_digits(q, E4M3) - q)
         assert np.all(e <= np.maximum(2.0 ** -20 * np.abs(q), 2.0 ** -32 * np.abs(q).max()))
+
+
+def test_the_border_query_tells_2_to_the_minus_22_from_half_of_it():
+    rng = np.random.default_rng(3)
+    q, signs = border_query(rng)
+    assert np.all(np.abs(query_digits(q, INT8) - q) <= 2.0 ** -22.9)
+    V, s = np.concatenate([np.full((1, D), 100.0), np.full((1, D), -100.0)]), np.ones(2)
+    K = 100.0 * np.stack([signs, -signs])
+    tol = bound_row(q, K, V, s, D ** -0.5, INT8)
+    out = softmax_row(q, K, V, D ** -0.5)[2]
+    assert np.all(np.abs(row_by_digits(q, K, V, s, D ** -0.5, INT8) - out) <= tol)
+    coarse = np.rint(q.astype(np.float64) * 2 ** 21) / 2 ** 21
+    assert np.all(np.abs(softmax_row(coarse, K, V, D ** -0.5)[2] - out) > tol)
