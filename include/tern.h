@@ -550,8 +550,8 @@ typedef struct tern_paged_cache {
  * in page pages[b * pages_ld + j / page_size].  A sequence may have no rows.
  * The arrays are device memory and read by the kernels, so a captured graph
  * serves changing lengths; T, and not the arrays, bounds every access to the
- * rows: rows from T on, and rows from row_start[B] on, are neither read nor
- * written.  max_rows and max_ctx only steer the choice of a kernel and its
+ * rows: rows from T on are neither read nor written, rows from row_start[B] on
+ * are not written, and what they and their positions hold does not matter.  max_rows and max_ctx only steer the choice of a kernel and its
  * split (a larger or smaller sequence is still computed right).
  */
 typedef struct tern_paged_batch {
@@ -637,7 +637,8 @@ tern_status tern_attention_paged_workspace_bytes(int32_t Hq, const tern_paged_ca
  * lengths: the same inputs give the same bits.  A query is held to 2^-22.9 of its
  * row's largest element (int8) or 2^-20 of each element (e4m3).  A softmax
  * weight times its block's value scale is held to 2^-27 of a reference (int8),
- * or to 2^-20 of itself and 2^-28 of the reference (e4m3).  The reference is
+ * or to 2^-20 of itself and 2^-28 of the reference (e4m3), where a scale below
+ * 2^-30 of the largest around it counts as that much.  The reference is
  * the row's largest such product so far; it falls to that of the present 128
  * tokens where theirs lies more than 2^12 below, in the tokens behind one that
  * stands out by 2^12 and else after 4096 to 8192 tokens (at most 2^48 in all):

@@ -15,8 +15,10 @@ constexpr int kPD = 128;                 // head dimension
 constexpr int kPB = TERN_KV_BLOCK;       // tokens that share a scale
 constexpr int kMaxBatch = 4096;          // sequences of a batch
 
-// Division of 0 <= n < 2^31 by a number fixed at the launch: multiply, add,
-// shift (with l = ceil(log2 d): mul = floor(2^32 (2^l - d) / d) + 1).
+// Division of 0 <= n < 2^31 by a number fixed at the launch, by the method of
+// Granlund and Montgomery (Division by Invariant Integers using Multiplication,
+// 1994): multiply, add, shift (with l = ceil(log2 d): mul = floor(2^32 (2^l - d)
+// / d) + 1).
 struct FastDiv {
     uint32_t d, mul, shift;
     __device__ __forceinline__ int quot(int n) const {

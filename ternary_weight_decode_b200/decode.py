@@ -20,9 +20,9 @@ the unfused form with separate act_quant_fwht launches ("unfused", 8 per
 layer) are kept for comparison and for M > 2.
 
 By default attention is not on this path (the pages give no detail) and its
-output is stood in by the q projection.  With ``attention="paged"`` it is: the
-M token rows are the next tokens of M sequences with an 8-bit paged KV cache
-(``PagedAttention`` below), and between steps 1 and 2 come
+output is stood in by the q projection.  With ``attention=PagedAttention(...)``
+it is: the M token rows are the next tokens of M sequences with an 8-bit paged
+KV cache, and between steps 1 and 2 come
 
   1a. tern_kv_append_paged(q, k, v of qkv)  -> q rotated, K and V into the cache
   1b. tern_attention_paged(q)               -> the input of Wo
@@ -30,7 +30,8 @@ M token rows are the next tokens of M sequences with an 8-bit paged KV cache
 Norms are not on this path; a weightless RMSNorm before each block is folded
 into s_x only (TERN_QUANT_RMSNORM), which leaves every int8 code unchanged and
 keeps the residual stream bounded over 64 layers.  Every step above runs in
-libtern's kernels.
+libtern's kernels; with attention, two torch additions a decode step advance
+the lengths and positions on the device.
 """
 from __future__ import annotations
 
@@ -104,7 +105,7 @@ class PagedAttention:
         self.ws = tern.attention_paged_workspace(self.Hq, self.caches[0])
         self.q = torch.zeros((M, self.Hq, self.head_dim), dtype=torch.float32, device="cuda")
         self.out = torch.zeros((M, hidden), dtype=torch.float32, device="cuda")
-        self.refused = torch.zeros(1, dtype=torch.int32, device="cuda")  # tokens past max_ctx (not appended)
+        self.refused = torch.zeros(1, dtype=torch.int32, device="cuda")  # tokens past max_ctx (not appended, or as 0)
         return self
 
     def set_ctx(self, ctx) -> None:
@@ -186,6 +187,7 @@ class DecodeModel:
         return self.n_layers * layer_bytes(self.fmt, self.hidden, self.qkv, self.ffn)
 
     def launches_per_step(self) -> int:
+        """libtern's launches (with attention, PagedAttention.advance adds two of torch's)."""
         n = {"streamed": 4 * self.n_layers, "fused": 4 * self.n_layers + 1, "unfused": 8 * self.n_layers}[self.mode]
         if self.attention is not None:  # append and attention; the fused form also needs the output's statistics
             n += (3 if self.mode == "fused" else 2) * self.n_layers

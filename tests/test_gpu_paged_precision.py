@@ -187,3 +187,34 @@ def test_queries_between_the_digits_steps(rows):
         see = 2 + r
         tol = bound_row(q[r, 0], K[:see], V[:see], s[:see], SCALE, INT8)
         assert np.all(np.abs(got[r, 0] - softmax_row(q[r, 0], K[:see], V[:see], SCALE)[2]) <= tol)
+
+
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("B,rows,Hq,ctx", [(148, 1, 4, 1500), (2, 1, 12, 700), (40, 5, 3, 1300), (1, 60, 2, 900), (148, 30, 1, 600)])
+@pytest.mark.parametrize("order", ["zeros first", "zeros between", "rising", "falling", "mixed"])
+def test_value_scales_far_apart(order, B, rows, Hq, ctx, kind):
+    """Values of tiles (or blocks) that differ by up to 2^26, and blocks of zeros, whose scale is the append's least."""
+    rng = np.random.default_rng(ctx + rows)
+    page = 128
+    n_pages = -(-ctx // page)
+    ref = appended(rng, kind, 1, page, n_pages)
+    pages = np.tile(np.arange(n_pages, dtype=np.int32), (B, 1))
+    t = np.arange(n_pages)[:, None] + np.zeros(8, int)
+    shift = {"zeros first": np.zeros_like(t), "zeros between": np.zeros_like(t), "rising": np.minimum(26, 5 * t),
+             "falling": -np.minimum(26, 5 * t), "mixed": rng.integers(-13, 14, t.shape)}[order]
+    ref["v_scales"][:, 0] *= np.exp2(shift).astype(np.float32)
+    zero = {"zeros first": t < 2, "zeros between": t % 3 == 1, "mixed": rng.random(t.shape) < 0.2}.get(order, t < 0)
+    ref["v_scales"][:, 0][zero] = 2.0 ** -100
+    ref["v_codes"].reshape(n_pages, 8, 16, D)[zero] = 0
+    dev = device_cache(ref, kind)
+    one = (rng.standard_normal((rows, Hq, D)) * 1.5).astype(np.float32)
+    start = np.arange(B + 1) * rows
+    got = run(np.tile(one, (B, 1, 1)), start, [ctx] * B, pages, dev, kind).reshape(B, rows, Hq, D)
+    K, V, s = (x[0] for x in sequence(ref, pages, 0, ctx, page, kind))
+    for r in range(0, rows, max(1, rows // 8)):
+        see = ctx - rows + r + 1
+        for h in range(Hq):
+            out = softmax_row(one[r, h], K[:see], V[:see], SCALE)[2]
+            tol = bound_row(one[r, h], K[:see], V[:see], s[:see], SCALE, kind)
+            err = np.abs(got[:, r, h] - out)
+            assert np.all(err <= tol), (r, h, err.max(), tol.min(), np.abs(out).max())
