@@ -39,8 +39,10 @@
 // item (26 of int8's 32 bits remain).
 // With weights and scales held by references of their own, a first token of a
 // large weight and a small value (what sinks are kept for) set both against
-// itself: at 65536 tokens, a score 2^27.5 above the rest and a value scale of
-// 1/64, what the others' weights lost was 6.6e-3 of the output.  So a reference
+// itself, and weights below 2^-27 of the one or scales' share of the other were
+// lost: at 65536 tokens and a value scale of 1/64, 2.3e-5 of the output (normal
+// scores, the first 2^24 above the largest), by a model up to 6.6e-3 (all others
+// 2^27.5 below).  So a reference
 // may fall as well: new references are taken from the present tile, wherever
 // that one's largest y lies 12 or more below the one that set m_r; and they are
 // taken behind a y that stands 12 above what came before it or above another 32
@@ -64,12 +66,14 @@
 // next item's digits while this one's tiles are worked off.
 //
 // Measured (device time; the floor is the codes at the measured copy rate): 24
-// sequences of up to 20011 tokens, 40 heads on 8, 97 us of 86 (int8 101; 16-token
-// pages); one of 65536 32.5 of 20.5, of 4096 12.9 of 1.3 (some 8 us are launch,
+// sequences of up to 20011 tokens, 40 heads on 8, 98 us of 86 (int8 103; 16-token
+// pages); one of 65536 35 of 20.5, of 4096 13 of 1.3 (some 8 us are launch,
 // look-up and the merging of divided items); 16 sequences of which a window and
-// sinks show 4100 tokens 34 of 20.7; three sequences of 16 drafted tokens 55 of
-// 8.0 and a prompt's 2048 rows of 4096 tokens 524 of 79: there some 20
-// instructions an element of the softmax, and the ends of items.
+// sinks show 4100 tokens 35 of 20.6; three sequences of 16 drafted tokens 60 of
+// 8.0 (e4m3 66) and a prompt's 2048 rows of 4096 tokens 525 of 79 (e4m3 1000):
+// there some 20 instructions an element of the softmax, and the ends of items.
+// All the loops together fill the instruction cache; a few hundred bytes more in
+// one of them have cost 5 to 25 %.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -1151,9 +1155,10 @@ cudaError_t launch_attention_paged(const PagedAttentionLaunch &A, cudaStream_t s
     const int64_t rows = std::min<int64_t>(static_cast<int64_t>(std::min(A.batch.max_rows, A.batch.T)) * p.GQ, 1 << 30);
     const bool int8 = A.cache.kind == TERN_KV_INT8;
     // Items of 8, 16 or, of int8, 32 rows (e4m3's digits take five columns of tensor memory a row).  In us with 8 / 16 /
-    // 32 rows, and e4m3 with 8 / 16: one token, context 65536, of 40 heads on 8 33.0 / - / 44.4, 34.2 / 36.5, of 128
-    // heads on 8 47.9 / 42.2 / 49.1; three sequences of 2 drafted tokens, 40 heads, context 8191 26.0 / 25.0 / 28.6, of
-    // 16 tokens 76 / 55 / 56, 80 / 62; a prompt's last 2048 of 4096 tokens 1042 / 780 / 539, 1149 / 1046.
+    // 32 rows, and e4m3 with 8 / 16: one token, context 65536, of 40 heads on 8 34.9 / 39.1 / 48.5, 33.6 / 39.4, of 128
+    // heads on 8 49.2 / 43.1 / 53.4, 52 / 44; three sequences of 2 drafted tokens, 40 heads, context 8191 27.6 / 26.3 /
+    // 33.1, 30.0 / 27.7, of 16 tokens 79 / 59 / 60, 84 / 66; a prompt's last 2048 of 4096 tokens 1078 / 862 / 525,
+    // 1300 / 1003.
     const int R = rows <= 8 ? 8 : int8 && rows > 16 ? 32 : 16;
     // one CTA per SM, fewer when the tiles are few
     const int64_t tiles = std::min<int64_t>(A.batch.B, A.batch.T) * A.cache.Hkv * ceil_div(rows, R) * ceil_div(span, kTok);
