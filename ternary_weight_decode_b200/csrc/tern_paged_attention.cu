@@ -99,6 +99,7 @@ constexpr int kChainInt8 = 32;            // tiles summed in int32, at most 256:
 constexpr int kChainE4m3 = 16;            // tiles summed in fp32 inside the tensor cores (16 or 64: the same time)
 constexpr float kFallBelow = 18.0f;       // a reference this far above a tile's largest product falls (12 below what set it)
 constexpr float kLowest = 48.0f;          // how far references may fall below the highest
+constexpr float kLowestAtOnce = 64.0f;    // and at once: tokens of far smaller value scales, as blocks of zeros have, may have set one
 constexpr int kScaleRange = 24;           // largest block scale of a tile (log2), relative to the item's
 constexpr int kScaleLowest = -30;         // least block scale that a reference is told apart by
 
@@ -933,7 +934,8 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
                     // far above what came before it, or what stands beside it
                     const float low = fminf(fminf(w0, w1), fminf(w2, w3));
                     far = (top > m + kHeadroom && m > -FLT_MAX) || (low < top - (kFallBelow - kHeadroom) && low > -FLT_MAX);
-                    if (top > m || (top < m - kFallBelow && top > -FLT_MAX)) m = fmaxf(top + kHeadroom, high - lowest);
+                    if (top > m || (top < m - kFallBelow && top > -FLT_MAX)) 
+                        m = fmaxf(fmaxf(top + kHeadroom, high - lowest), was - kLowestAtOnce);
                     *mp = m;
                     *hp = fmaxf(high, m);
                     reinterpret_cast<float *>(S.back[g])[gt] = ex2(was - m);
@@ -1024,7 +1026,8 @@ __global__ void __launch_bounds__(Shape<R, KIND>::kThreads, 1)
 #pragma unroll
                 for (int r = 0; r < kRW; ++r) own[(r0 + r) * kPD] = o[r];
                 any_of<kGroup>(false, g);
-                const float zr = gt < R ? (S.zsum[g][0][gt] + S.zsum[g][1][gt]) + (S.zsum[g][2][gt] + S.zsum[g][3][gt]) : 0.0f;
+                float zr = gt < R ? (S.zsum[g][0][gt] + S.zsum[g][1][gt]) + (S.zsum[g][2][gt] + S.zsum[g][3][gt]) : 0.0f;
+                if (zr > FLT_MAX) zr = FLT_MAX;  // (of references that fell twice by the most; its output is 0 all the same)
                 if (hand) {
                     if (gt < R) {
                         S.sum_z[gt] = zr;

@@ -218,3 +218,34 @@ def test_value_scales_far_apart(order, B, rows, Hq, ctx, kind):
             tol = bound_row(one[r, h], K[:see], V[:see], s[:see], SCALE, kind)
             err = np.abs(got[:, r, h] - out)
             assert np.all(err <= tol), (r, h, err.max(), tol.min(), np.abs(out).max())
+
+
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("above", [60.0, 130.0, 300.0])
+@pytest.mark.parametrize("zeros", [16, 128, 256])
+@pytest.mark.parametrize("B", [1, 148])
+def test_zeros_far_above_the_rest(B, zeros, above, kind):
+    """A first token 2^above over the others whose block, or whose first tiles, have values of 0: the output is finite, and
+    nothing but what the others' weights leave of their values."""
+    rng = np.random.default_rng(zeros)
+    page, ctx, Hq = 128, 1000, 3
+    n_pages = -(-ctx // page)
+    ref = appended(rng, kind, 1, page, n_pages)
+    flat = ref["v_codes"].reshape(n_pages * page, D)
+    flat[:zeros] = 0
+    ref["v_scales"].reshape(-1)[:zeros // 16] = 2.0 ** -100
+    ref["k_codes"][0, 0, 0] = paged.to_codes((rng.choice([-1.0, 1.0], D) * 100).astype(np.float32), kind)
+    ref["k_scales"][0, 0, 0] = np.float32(2.0 ** -4)
+    pages = np.tile(np.arange(n_pages, dtype=np.int32), (B, 1))
+    K, V, s = (x[0] for x in sequence(ref, pages, 0, ctx, page, kind))
+    q = rng.standard_normal((Hq, D)) * 0.5
+    for h in range(Hq):
+        for _ in range(60):
+            x = K @ q[h] * (SCALE * np.log2(np.e))
+            q[h] += K[0] / (K[0] @ K[0]) * (above - (x[0] - x[1:].max())) / (SCALE * np.log2(np.e))
+    q = q.astype(np.float32)
+    got = run(np.tile(q, (B, 1, 1)), np.arange(B + 1), [ctx] * B, pages, device_cache(ref, kind), kind)
+    assert np.all(np.isfinite(got))
+    # a weight 2^-above of the first's, at most; it may be off by all of itself where it lies below what is kept
+    most = min(1.0, ctx * 2.0 ** (1 - above)) * np.abs(V).max()
+    assert np.all(np.abs(got) <= most)
