@@ -573,7 +573,7 @@ _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cud
 class _Described:
     """A descriptor whose C struct is kept until a field is replaced, or one of
     ``probes`` (where its tensors lie, and what may change in place) answers
-    otherwise."""
+    otherwise.  ``sizes``: the struct's fields that the calls below go by."""
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
@@ -583,12 +583,13 @@ class _Described:
         return {k: v for k, v in self.__dict__.items() if k != "_kept"}
 
     def described(self):
-        """(address of the struct, device index, the struct).  Whoever passes the address on holds the
-        tuple until the call has returned: another thread may meanwhile have a new struct made."""
+        """(address of the struct, device index, its ``sizes``, the struct).  Whoever passes the address on
+        holds the struct until the call has returned: another thread may meanwhile have a new one made."""
         kept = self.__dict__.get("_kept")
         if kept is None or [f() for f in kept[1]] != kept[2]:
             s, probes = self.struct(), self.probes()
-            kept = ((ctypes.addressof(s), self.device_index(), s), probes, [f() for f in probes])
+            kept = ((ctypes.addressof(s), self.device_index(), tuple(getattr(s, n) for n in self.sizes), s), probes,
+                    [f() for f in probes])
             self.__dict__["_kept"] = kept
         return kept[0]
 
@@ -621,7 +622,7 @@ def _heads(t: torch.Tensor, dev: int, T: int, H: int, D: int) -> int:
 def _positions(t: torch.Tensor, dev: int, axes: int, T: int) -> int:
     if t.get_device() != dev:
         raise ValueError(f"pos is on {t.device}, the others are on cuda:{dev}")
-    assert t.dtype == torch.int32 and t.shape == (axes, T) and t.is_contiguous(), (t.dtype, tuple(t.shape))
+    assert t.dtype is torch.int32 and t.shape == (axes, T) and t.is_contiguous(), (t.dtype, tuple(t.shape))
     return t.data_ptr()
 
 
@@ -642,6 +643,7 @@ class RopePlan(_Described):
     sections: tuple | list | None = None
     interleaved: bool = False
     inverse: bool = False
+    sizes = ("axes",)
 
     @property
     def axes(self) -> int:
@@ -684,8 +686,8 @@ def tern_rope_table(theta: float, scale: float, table: torch.Tensor, stream=None
 def tern_rope(rope: RopePlan, pos: torch.Tensor, x: torch.Tensor, y: torch.Tensor, d_invalid=None, stream=None):
     """y [T, H, D] = x rotated by pos int32 [axes, T]; y may be x."""
     T, H, D = x.shape
-    plan, dev, r = rope.described()
-    st = (_lib or lib()).tern_rope(plan, _positions(pos, dev, r.axes, T), T, H, D, x.data_ptr(),
+    plan, dev, (axes,), _struct = rope.described()
+    st = (_lib or lib()).tern_rope(plan, _positions(pos, dev, axes, T), T, H, D, x.data_ptr(),
                                    _heads(x, dev, T, H, D), y.data_ptr(), _heads(y, dev, T, H, D),
                                    _counter(d_invalid, dev), _call_stream(dev, stream))
     if st:
@@ -704,6 +706,7 @@ class PagedCache(_Described):
     k_scales: torch.Tensor
     v_codes: torch.Tensor
     v_scales: torch.Tensor
+    sizes = ("Hkv", "D")
 
     @staticmethod
     def empty(kind: int, Hkv: int, D: int, page_size: int, n_pages: int, device="cuda") -> "PagedCache":
@@ -743,6 +746,7 @@ class PagedBatch(_Described):
     T: int
     max_rows: int
     max_ctx: int
+    sizes = ("T",)
 
     def device_index(self) -> int:
         return _one_device(self.row_start, self.ctx, self.pages)
@@ -771,14 +775,14 @@ def tern_kv_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos:
                          batch: PagedBatch, cache: PagedCache, q_out: torch.Tensor, d_invalid=None, stream=None):
     """q_out [T, Hq, D] = q rotated; k (rotated) and v [T, Hkv, D] quantised into the cache.
     pos int32 [axes, T]; q_out may be q."""
-    (b, dev, bs), (c, _, cs) = _batch_and_cache(batch, cache)
-    plan, dev_r, r = rope.described()
-    T, Hq, Hkv, D = bs.T, q.shape[1], cs.Hkv, cs.D
+    (b, dev, (T,), _b), (c, _, (Hkv, D), _c) = _batch_and_cache(batch, cache)
+    plan, dev_r, (axes,), _r = rope.described()
+    Hq = q.shape[1]
     if dev_r != dev:
         raise ValueError(f"the rotary table is on cuda:{dev_r}, the batch on cuda:{dev}")
     st = (_lib or lib()).tern_kv_append_paged(
         q.data_ptr(), _heads(q, dev, T, Hq, D), Hq, k.data_ptr(), _heads(k, dev, T, Hkv, D), v.data_ptr(),
-        _heads(v, dev, T, Hkv, D), _positions(pos, dev, r.axes, T), plan, b, c, q_out.data_ptr(),
+        _heads(v, dev, T, Hkv, D), _positions(pos, dev, axes, T), plan, b, c, q_out.data_ptr(),
         _heads(q_out, dev, T, Hq, D), _counter(d_invalid, dev), _call_stream(dev, stream))
     if st:
         _check(st, "tern_kv_append_paged")
@@ -787,8 +791,7 @@ def tern_kv_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos:
 def tern_kv_read_paged(batch: PagedBatch, cache: PagedCache, k_out: torch.Tensor, v_out: torch.Tensor,
                        d_invalid=None, stream=None):
     """k_out, v_out [T, Hkv, D] = the cache's values of the batch's rows."""
-    (b, dev, bs), (c, _, cs) = _batch_and_cache(batch, cache)
-    T, H, D = bs.T, cs.Hkv, cs.D
+    (b, dev, (T,), _b), (c, _, (H, D), _c) = _batch_and_cache(batch, cache)
     st = (_lib or lib()).tern_kv_read_paged(b, c, k_out.data_ptr(), _heads(k_out, dev, T, H, D), v_out.data_ptr(),
                                             _heads(v_out, dev, T, H, D), _counter(d_invalid, dev),
                                             _call_stream(dev, stream))
@@ -798,7 +801,7 @@ def tern_kv_read_paged(batch: PagedBatch, cache: PagedCache, k_out: torch.Tensor
 
 def tern_attention_paged_workspace_bytes(Hq: int, cache: PagedCache) -> int:
     n = ctypes.c_size_t()
-    c, dev, _struct = cache.described()
+    c, dev, _, _struct = cache.described()
     _call_stream(dev, None)  # (the answer is the current device's)
     _check(lib().tern_attention_paged_workspace_bytes(Hq, c, ctypes.byref(n)),
            "tern_attention_paged_workspace_bytes")
@@ -817,8 +820,8 @@ def tern_attention_paged(q: torch.Tensor, batch: PagedBatch, cache: PagedCache, 
                          stream=None):
     """out [T, Hq, D] = causal attention of the batch's rows q over the cache;
     window tokens (0: all) and the first `sinks` are visible; scale 1/sqrt(D) by default."""
-    (b, dev, bs), (c, _, cs) = _batch_and_cache(batch, cache)
-    T, Hq, D = bs.T, q.shape[1], cs.D
+    (b, dev, (T,), _b), (c, _, (_, D), _c) = _batch_and_cache(batch, cache)
+    Hq = q.shape[1]
     if workspace.get_device() != dev:
         raise ValueError(f"the workspace is on {workspace.device}, the batch on cuda:{dev}")
     assert workspace.is_contiguous()

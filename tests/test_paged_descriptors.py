@@ -134,20 +134,20 @@ def test_tensors_resized_together_are_followed(tern):
     batch.row_start.resize_(2), batch.ctx.resize_(1), batch.pages.resize_(1, 2)
     plan.table.resize_(8, 32, 2)
     plan.sections[:] = [20, 12]
-    assert cache.described()[2].n_pages == 2
-    assert (batch.described()[2].B, batch.described()[2].pages_ld) == (1, 2)
-    assert plan.described()[2].rot_dim == 64
+    assert cache.described()[3].n_pages == 2
+    assert (batch.described()[3].B, batch.described()[3].pages_ld) == (1, 2)
+    assert plan.described()[3].rot_dim == 64
     plan.table.resize_(4, 64, 2)   # the same number of elements
-    assert (plan.described()[2].n_pos, plan.described()[2].rot_dim) == (4, 128)
+    assert (plan.described()[3].n_pos, plan.described()[3].rot_dim) == (4, 128)
 
 
 @pytest.mark.parametrize("copied", [copy.copy, copy.deepcopy, lambda d: pickle.loads(pickle.dumps(d))])
 def test_descriptors_that_were_used_are_copied(tern, copied):
     for d in descriptors(tern):
-        address, _, kept = d.described()
+        address, _, _, kept = d.described()
         other = copied(d)
         assert type(other) is type(d) and "_kept" not in other.__dict__
-        assert other.described()[0] != address and d.described()[2] is kept
+        assert other.described()[0] != address and d.described()[3] is kept
         for name, t in other.__dict__.items():
             if isinstance(t, torch.Tensor):
                 assert torch.equal(t, getattr(d, name))
